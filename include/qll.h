@@ -17,7 +17,12 @@
  *                               CDNA4 matrix cores (see below)
  *   quantize_int4_weights,      INT4 weight-only: symmetric int4 weights with a
  *   gemm_w4a16                  scale per 128-element group, bf16 activations
- * Each GEMM runs as an ordinary tiled GEMM, as Split-K or as Swap-AB (the
+ *   gemm_bf16_epilogue,         products with bias, activation and residual,
+ *   gemm_fp8_epilogue           and the bf16 backward pass
+ *   gated_bf16, gated_fp8       gated projections, and the bf16 backward pass
+ *   residual_norm               post-norm, gate, residual and pre-norm (bf16 or
+ *                               e4m3 out), and the backward pass
+ * Each scaled GEMM runs as an ordinary tiled GEMM, as Split-K or as Swap-AB (the
  * three strategies of "What the integration changes"), chosen per (M, N, K)
  * by a dispatch table that an on-device sweep fills, or forced with the _ex
  * entry points.
@@ -312,6 +317,112 @@ int gemm_fp8_grouped_ex(const void* A, const void* B, const float* sa, const flo
  * a NUL-terminated name into buf (cap bytes).  INVALID_ARG on bad arguments
  * or a too small buffer. */
 int qll_grouped_select(int64_t M, int64_t E, char* buf, size_t cap);
+
+/* ------------------------------------------------------------------ */
+/* Feed-forward operators                                              */
+/* ------------------------------------------------------------------ */
+
+/* What stands around and between a feed-forward block's linear layers, with
+ * the library's conventions (dense row-major device pointers, 16-byte aligned
+ * tensors and vectors, 4-byte aligned fp32 scales and vector gradients).
+ * Everything is computed in fp32 and rounded once per output; intermediate
+ * roundings are stated where there are any.  The feed-forward operators take
+ * rows of up to 8388607 bytes (UNSUPPORTED beyond).
+ *
+ * Activations, f(z): */
+typedef enum {
+    QLL_ACT_NONE = 0,
+    QLL_ACT_RELU = 1,
+    QLL_ACT_GELU = 2,      /* z Phi(z), the erf form */
+    QLL_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    QLL_ACT_SILU = 4,      /* z / (1 + e^-z) */
+    QLL_ACT_SIGMOID = 5    /* 1 / (1 + e^-z) */
+} qll_act;
+
+/* Matrix product with bias, activation and residual in its epilogue:
+ *   out[m][n] = act(sum_k A[m][k] B[n][k] + bias[n]) + residual[m][n]
+ *   (fp8: the sum is ((sum_k ..) sa[m]) sb[n], as in gemm_fp8_scaled)
+ *   A [M][K], B [N][K]: bf16 (K % 8 == 0) or e4m3 (K % 16 == 0); sa fp32 [M],
+ *   sb fp32 [N]; bias bf16 [N] or NULL; residual bf16 [M][N] or NULL (may be
+ *   `out` itself when out is bf16); out bf16 / fp32 [M][N].  Any N.
+ * ws: qll_epilogue_workspace_bytes(fp8, M, N, K) bytes, 16-byte aligned
+ * (Split-K of shapes with few output tiles; 0 for most).  M == 0 is a no-op. */
+int gemm_bf16_epilogue(const void* A, const void* B, const void* bias, const void* residual,
+                       int act, void* out, int out_dtype, int64_t M, int64_t N, int64_t K,
+                       void* ws, size_t ws_bytes, void* stream);
+int gemm_fp8_epilogue(const void* A, const void* B, const float* sa, const float* sb,
+                      const void* bias, const void* residual, int act, void* out,
+                      int out_dtype, int64_t M, int64_t N, int64_t K, void* ws,
+                      size_t ws_bytes, void* stream);
+int64_t qll_epilogue_workspace_bytes(int fp8, int64_t M, int64_t N, int64_t K);
+
+/* Its backward pass (bf16; the residual's gradient is dout itself):
+ *   z = A B^T + bias (computed again when act != NONE), dz = dout act'(z)
+ *   dA = dz B,  dB = dz^T A,  dbias[n] = sum_m dz[m][n]
+ *   (relu'(0) = 0).  dz is rounded to bf16 for the two products, and not for
+ *   dbias.  dout bf16 [M][N]; dA bf16 [M][K], dB bf16 [N][K], dbias fp32 [N],
+ *   each NULL if not wanted.  K % 8 == 0, N % 8 == 0.
+ *   M == 0 writes zeros to dB and dbias.
+ * ws: qll_epilogue_backward_workspace_bytes(act, dbias != NULL, M, N, K). */
+int gemm_bf16_epilogue_backward(const void* A, const void* B, const void* dout,
+                                const void* bias, int act, void* dA, void* dB, float* dbias,
+                                int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                                void* stream);
+int64_t qll_epilogue_backward_workspace_bytes(int act, int has_bias, int64_t M, int64_t N,
+                                              int64_t K);
+
+/* Gated projections, both products, the activation and the product of the two
+ * in one kernel:
+ *   out[m][n] = act(g) u,  g = sum_k A[m][k] Bg[n][k],  u = sum_k A[m][k] Bu[n][k]
+ *   (fp8: g scaled by sa[m] sg[n], u by sa[m] su[n])
+ *   A [M][K]; Bg, Bu [N][K]: bf16 (K % 8 == 0) or e4m3 (K % 16 == 0); out
+ *   bf16 / fp32 [M][N].  Any N.  No workspace.  M == 0 is a no-op. */
+int gated_bf16(const void* A, const void* Bg, const void* Bu, int act, void* out,
+               int out_dtype, int64_t M, int64_t N, int64_t K, void* stream);
+int gated_fp8(const void* A, const void* Bg, const void* Bu, const float* sa, const float* sg,
+              const float* su, int act, void* out, int out_dtype, int64_t M, int64_t N,
+              int64_t K, void* stream);
+
+/* Its backward pass (bf16); g and u are computed again from A, so the forward
+ * pass keeps nothing:
+ *   dg = dout u act'(g),  du = dout act(g)   (both rounded to bf16)
+ *   dA = dg Bg + du Bu,  dBg = dg^T A,  dBu = du^T A
+ *   dA bf16 [M][K], or NULL; dBg, dBu bf16 [N][K], or both NULL.
+ *   K % 8 == 0, N % 8 == 0.  M == 0 writes zeros to dBg and dBu.
+ * ws: qll_gated_backward_workspace_bytes(M, N, K). */
+int gated_bf16_backward(const void* A, const void* Bg, const void* Bu, const void* dout,
+                        int act, void* dA, void* dBg, void* dBu, int64_t M, int64_t N,
+                        int64_t K, void* ws, size_t ws_bytes, void* stream);
+int64_t qll_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Residual norms: a block's output joins the residual stream through its
+ * post-norm, channel gate and scales, and the next block's pre-norm follows.
+ *   p = y / rms(y) w_post  (w_post NULL: y),  rms(v) = sqrt(mean(v^2) + eps)
+ *   h = alpha r + beta gate p  (gate NULL: 1)
+ *   n = h / rms(h) w_pre
+ *   y bf16 [M][K]; r [M][K] bf16 or fp32 (r_dtype, QLL_OUT_BF16 or _FP32);
+ *   w_post, gate, w_pre bf16 [K]; r_out = h, of r's type (may be r itself);
+ *   n_out bf16 [M][K], or with n_scales e4m3 [M][K] and fp32 [M] by the rule
+ *   of quantize_per_token_fp8 (applied to the fp32 n).  n uses h unrounded.
+ *   y NULL: h = r (alpha 1, w_post, gate and r_out NULL).
+ *   K % 8 == 0 (16 for e4m3), K <= 32768.  M == 0 is a no-op. */
+int residual_norm(const void* y, const void* r, int r_dtype, const void* w_post,
+                  const void* gate, const void* w_pre, float alpha, float beta, float eps,
+                  void* r_out, void* n_out, float* n_scales, int64_t M, int64_t K,
+                  void* stream);
+
+/* Its backward pass, from y and r (h and the norms are computed again), the
+ * gradient dn of n (bf16) and dr_out of h (type of r, or NULL for zero):
+ * dy bf16 [M][K] (NULL without y), dr [M][K] of r's type, and the vector
+ * gradients dw_post, dgate (NULL where the vector is) and dw_pre, fp32 [K].
+ * M == 0 writes zeros to the vector gradients.
+ * ws: qll_residual_norm_backward_workspace_bytes(M, K). */
+int residual_norm_backward(const void* y, const void* r, int r_dtype, const void* w_post,
+                           const void* gate, const void* w_pre, float alpha, float beta,
+                           float eps, const void* dn, const void* dr_out, void* dy, void* dr,
+                           float* dw_post, float* dgate, float* dw_pre, int64_t M, int64_t K,
+                           void* ws, size_t ws_bytes, void* stream);
+int64_t qll_residual_norm_backward_workspace_bytes(int64_t M, int64_t K);
 
 /* ------------------------------------------------------------------ */
 /* Without device allocation                                           */

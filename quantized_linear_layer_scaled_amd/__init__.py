@@ -16,7 +16,12 @@ Operations (see include/qll.h for the full contract):
   quantize_mxfp4, gemm_mxfp4 (MXFP4: E2M1 codes packed two per byte, one
   E8M0 scale byte per 32 elements of a row; tensors as uint8),
   quantize_int4_weights, gemm_w4a16 (INT4 weight-only: int4 codes packed two
-  per byte, an fp32 scale per 128-element group, bf16 activations).
+  per byte, an fp32 scale per 128-element group, bf16 activations),
+  gemm_bf16_epilogue, gemm_fp8_epilogue (bias, activation and residual in the
+  epilogue) and gemm_bf16_epilogue_backward,
+  gated_bf16, gated_fp8 (act(x Bg^T) * (x Bu^T)) and gated_bf16_backward,
+  residual_norm, residual_norm_backward (post-norm, gate, residual stream and
+  pre-norm in one pass).
 """
 from __future__ import annotations
 
@@ -35,6 +40,7 @@ STATUS = {0: "QLL_OK", 1: "QLL_ERR_INVALID_ARG", 2: "QLL_ERR_UNSUPPORTED",
 OUT = {"bf16": 0, "fp32": 1, "int32": 2}
 OPS = {"int8": 0, "fp8": 1, "block_fp8": 2, "bf16_bi": 3, "mxfp4": 4, "w4a16": 5,
        "fp8_dynamic": 6}
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
 
 
 class QllError(RuntimeError):
@@ -92,6 +98,23 @@ def load_library():
                                      ctypes.c_int, ctypes.c_char_p, ctypes.c_char_p,
                                      ctypes.c_size_t]
     L.qll_device_signature.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
+    _I, _Z, _F = ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    _MNK = [_I64, _I64, _I64]
+    L.gemm_bf16_epilogue.argtypes = [_P] * 4 + [_I, _P, _I] + _MNK + [_P, _Z, _P]
+    L.gemm_fp8_epilogue.argtypes = [_P] * 6 + [_I, _P, _I] + _MNK + [_P, _Z, _P]
+    L.gemm_bf16_epilogue_backward.argtypes = [_P] * 4 + [_I] + [_P] * 3 + _MNK + [_P, _Z, _P]
+    L.gated_bf16.argtypes = [_P] * 3 + [_I, _P, _I] + _MNK + [_P]
+    L.gated_fp8.argtypes = [_P] * 6 + [_I, _P, _I] + _MNK + [_P]
+    L.gated_bf16_backward.argtypes = [_P] * 4 + [_I] + [_P] * 3 + _MNK + [_P, _Z, _P]
+    L.residual_norm.argtypes = [_P, _P, _I] + [_P] * 3 + [_F] * 3 + [_P] * 3 + [_I64, _I64, _P]
+    L.residual_norm_backward.argtypes = ([_P, _P, _I] + [_P] * 3 + [_F] * 3 + [_P] * 7 +
+                                         [_I64, _I64, _P, _Z, _P])
+    L.qll_epilogue_workspace_bytes.argtypes = [_I] + _MNK
+    L.qll_epilogue_backward_workspace_bytes.argtypes = [_I, _I] + _MNK
+    L.qll_gated_backward_workspace_bytes.argtypes = _MNK
+    L.qll_residual_norm_backward_workspace_bytes.argtypes = [_I64, _I64]
+    for name in ("epilogue", "epilogue_backward", "gated_backward", "residual_norm_backward"):
+        getattr(L, f"qll_{name}_workspace_bytes").restype = _I64
     L.gemm_fp8_scaled_noalloc.argtypes = _GEMM_ARGS[:9] + [_P]
     L.qll_select.argtypes = [ctypes.c_int, _I64, _I64, _I64, ctypes.POINTER(qll_cfg)]
     L.qll_workspace_bytes.argtypes = [ctypes.c_int, _I64, _I64, _I64,
@@ -534,6 +557,301 @@ def grouped_select(M: int, E: int) -> str:
     buf = ctypes.create_string_buffer(64)
     _check("qll_grouped_select", load_library().qll_grouped_select(M, E, buf, 64))
     return buf.value.decode()
+
+
+# --------------------------------------------------------------------------
+# feed-forward operators
+# --------------------------------------------------------------------------
+
+def _ffn_device(stream, **tensors):
+    """The operators launch on the current device: every tensor (and the
+    stream, if given) has to be there."""
+    torch = _torch()
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        if t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    if stream is not None and stream.device.index != here:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{here}")
+
+
+def _typed(t, name, dtype, shape):
+    """Pointer of a contiguous tensor of this type and shape, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return _dev_ptr(t, name)
+
+
+def _act(act):
+    if act not in ACT:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACT)}")
+    return ACT[act]
+
+
+def _float_out(out, M, N, out_dtype, device):
+    if out_dtype not in ("bf16", "fp32"):
+        raise ValueError("out_dtype must be 'bf16' or 'fp32'")
+    return _out(out, M, N, out_dtype, device)
+
+
+def _scratch(query, need, workspace, device):
+    """(workspace, bytes) of at least `need` bytes, allocated if not given."""
+    torch = _torch()
+    if need < 0:
+        raise QllError(query, -need)
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _dev_ptr(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape
+
+
+def _epilogue(fp8, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace, stream):
+    torch = _torch()
+    _ffn_device(stream, A=A, B=B, sa=sa, sb=sb, bias=bias, residual=residual, out=out,
+                workspace=workspace)
+    M, K = _matrix(A, "A")
+    N, K2 = _matrix(B, "B")
+    if K2 != K:
+        raise ValueError(f"A is [M][{K}] but B is [N][{K2}]")
+    code = _act(act)
+    L = load_library()
+    bf = torch.bfloat16
+    args = ([_bytes8(A, "A"), _bytes8(B, "B"), _f32(sa, "sa", (M,)), _f32(sb, "sb", (N,))] if fp8
+            else [_typed(A, "A", bf, (M, K)), _typed(B, "B", bf, (N, K))])
+    args += [_typed(bias, "bias", bf, (N,)), _typed(residual, "residual", bf, (M, N)), code]
+    with _on(stream):
+        out = _float_out(out, M, N, out_dtype, A.device)
+        ws, wsb = _scratch("qll_epilogue_workspace_bytes",
+                           L.qll_epilogue_workspace_bytes(int(fp8), M, N, K), workspace, A.device)
+        fn = "gemm_fp8_epilogue" if fp8 else "gemm_bf16_epilogue"
+        rc = getattr(L, fn)(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K, _ptr(ws), wsb,
+                            _stream(stream))
+    _check(fn, rc)
+    return out
+
+
+def gemm_bf16_epilogue(A, B, bias=None, residual=None, act="none", out_dtype="bf16", out=None,
+                       workspace=None, stream=None):
+    """act(A B^T + bias) + residual: bf16 A [M][K], B [N][K], bias [N],
+    residual [M][N]."""
+    return _epilogue(False, A, B, None, None, bias, residual, act, out_dtype, out, workspace, stream)
+
+
+def gemm_fp8_epilogue(A, B, sa, sb, bias=None, residual=None, act="none", out_dtype="bf16",
+                      out=None, workspace=None, stream=None):
+    """act((A B^T) sa sb + bias) + residual: e4m3 A [M][K], B [N][K], fp32 sa
+    [M], sb [N], bf16 bias [N], residual [M][N]."""
+    return _epilogue(True, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace, stream)
+
+
+def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=True,
+                                need_weight=True, dA=None, dB=None, dbias=None, workspace=None,
+                                stream=None):
+    """(dA, dB, dbias) of gemm_bf16_epilogue for bf16 dout [M][N] (the
+    residual's gradient is dout itself): dA bf16 [M][K], dB bf16 [N][K], dbias
+    fp32 [N]; None for what is not needed (dbias without a bias)."""
+    torch = _torch()
+    _ffn_device(stream, A=A, B=B, dout=dout, bias=bias, dA=dA, dB=dB, dbias=dbias,
+                workspace=workspace)
+    M, K = _matrix(A, "A")
+    N, K2 = _matrix(B, "B")
+    if K2 != K:
+        raise ValueError(f"A is [M][{K}] but B is [N][{K2}]")
+    code = _act(act)
+    if not (need_input or need_weight or bias is not None):
+        raise ValueError("nothing to compute")
+    L = load_library()
+    bf = torch.bfloat16
+    args = [_typed(A, "A", bf, (M, K)), _typed(B, "B", bf, (N, K)),
+            _typed(dout, "dout", bf, (M, N)), _typed(bias, "bias", bf, (N,)), code]
+    with _on(stream):
+        if need_input and dA is None:
+            dA = torch.empty_like(A)
+        if need_weight and dB is None:
+            dB = torch.empty_like(B)
+        if bias is not None and dbias is None:
+            dbias = torch.empty(N, dtype=torch.float32, device=A.device)
+        dA, dB = dA if need_input else None, dB if need_weight else None
+        dbias = dbias if bias is not None else None
+        need = L.qll_epilogue_backward_workspace_bytes(code, int(dbias is not None), M, N, K)
+        ws, wsb = _scratch("qll_epilogue_backward_workspace_bytes", need, workspace, A.device)
+        rc = L.gemm_bf16_epilogue_backward(
+            *args, _typed(dA, "dA", bf, (M, K)), _typed(dB, "dB", bf, (N, K)),
+            _typed(dbias, "dbias", torch.float32, (N,)), M, N, K, _ptr(ws), wsb, _stream(stream))
+    _check("gemm_bf16_epilogue_backward", rc)
+    return dA, dB, dbias
+
+
+def _gated_sizes(A, Bg, Bu):
+    M, K = _matrix(A, "A")
+    N, K2 = _matrix(Bg, "Bg")
+    if K2 != K or tuple(Bu.shape) != (N, K):
+        raise ValueError(f"A is [M][{K}] but Bg is {tuple(Bg.shape)} and Bu {tuple(Bu.shape)}")
+    return M, N, K
+
+
+def gated_bf16(A, Bg, Bu, act="silu", out_dtype="bf16", out=None, stream=None):
+    """act(A Bg^T) * (A Bu^T): bf16 A [M][K], Bg and Bu [N][K]."""
+    torch = _torch()
+    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, out=out)
+    M, N, K = _gated_sizes(A, Bg, Bu)
+    bf = torch.bfloat16
+    args = [_typed(A, "A", bf, (M, K)), _typed(Bg, "Bg", bf, (N, K)),
+            _typed(Bu, "Bu", bf, (N, K)), _act(act)]
+    with _on(stream):
+        out = _float_out(out, M, N, out_dtype, A.device)
+        rc = load_library().gated_bf16(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K,
+                                       _stream(stream))
+    _check("gated_bf16", rc)
+    return out
+
+
+def gated_fp8(A, Bg, Bu, sa, sg, su, act="silu", out_dtype="bf16", out=None, stream=None):
+    """act((A Bg^T) sa sg) * ((A Bu^T) sa su): e4m3 A [M][K], Bg and Bu
+    [N][K], fp32 sa [M], sg and su [N]."""
+    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, sa=sa, sg=sg, su=su, out=out)
+    M, N, K = _gated_sizes(A, Bg, Bu)
+    args = [_bytes8(A, "A"), _bytes8(Bg, "Bg"), _bytes8(Bu, "Bu"), _f32(sa, "sa", (M,)),
+            _f32(sg, "sg", (N,)), _f32(su, "su", (N,)), _act(act)]
+    with _on(stream):
+        out = _float_out(out, M, N, out_dtype, A.device)
+        rc = load_library().gated_fp8(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K,
+                                      _stream(stream))
+    _check("gated_fp8", rc)
+    return out
+
+
+def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weight=True, dA=None,
+                        dBg=None, dBu=None, workspace=None, stream=None):
+    """(dA, dBg, dBu) of gated_bf16 for bf16 dout [M][N], all bf16; None for
+    what is not needed."""
+    torch = _torch()
+    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, dout=dout, dA=dA, dBg=dBg, dBu=dBu, workspace=workspace)
+    M, N, K = _gated_sizes(A, Bg, Bu)
+    if not (need_input or need_weight):
+        raise ValueError("nothing to compute")
+    L = load_library()
+    bf = torch.bfloat16
+    args = [_typed(A, "A", bf, (M, K)), _typed(Bg, "Bg", bf, (N, K)), _typed(Bu, "Bu", bf, (N, K)),
+            _typed(dout, "dout", bf, (M, N)), _act(act)]
+    with _on(stream):
+        dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
+        dBg = (torch.empty_like(Bg) if dBg is None else dBg) if need_weight else None
+        dBu = (torch.empty_like(Bu) if dBu is None else dBu) if need_weight else None
+        need = L.qll_gated_backward_workspace_bytes(M, N, K)
+        ws, wsb = _scratch("qll_gated_backward_workspace_bytes", need, workspace, A.device)
+        rc = L.gated_bf16_backward(
+            *args, _typed(dA, "dA", bf, (M, K)), _typed(dBg, "dBg", bf, (N, K)),
+            _typed(dBu, "dBu", bf, (N, K)), M, N, K, _ptr(ws), wsb, _stream(stream))
+    _check("gated_bf16_backward", rc)
+    return dA, dBg, dBu
+
+
+def _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps):
+    torch = _torch()
+    bf = torch.bfloat16
+    M, K = _matrix(r, "r")
+    if r.dtype not in (bf, torch.float32):
+        raise ValueError("r must be bfloat16 or float32")
+    if y is None and (w_post is not None or gate is not None or alpha != 1.0):
+        raise ValueError("w_post, gate and alpha need a block output y")
+    kind = OUT["bf16"] if r.dtype == bf else OUT["fp32"]
+    return M, K, [_typed(y, "y", bf, (M, K)), _dev_ptr(r, "r"), kind,
+                  _typed(w_post, "w_post", bf, (K,)), _typed(gate, "gate", bf, (K,)),
+                  _typed(w_pre, "w_pre", bf, (K,)), alpha, beta, eps]
+
+
+def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
+                  quantize=False, r_out=None, n_out=None, scales=None, stream=None):
+    """Residual stream and pre-norm behind a block: h = alpha r + beta gate *
+    (w_post y / rms(y)), n = w_pre h / rms(h).  y bf16 [M][K] (None: h = r), r
+    bf16 or fp32 [M][K], vectors bf16 [K].  Returns (h, n) with n bf16, or with
+    quantize (h, e4m3 codes, fp32 scales [M][1]).  r_out may be r."""
+    torch = _torch()
+    _ffn_device(stream, y=y, r=r, w_pre=w_pre, w_post=w_post, gate=gate, r_out=r_out, n_out=n_out,
+                scales=scales)
+    M, K, args = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps)
+    with _on(stream):
+        if y is None:
+            if r_out is not None:
+                raise ValueError("without y the stream is r itself")
+        elif r_out is None:
+            r_out = torch.empty_like(r)
+        ndt = torch.float8_e4m3fn if quantize else torch.bfloat16
+        if n_out is None:
+            n_out = torch.empty((M, K), dtype=ndt, device=r.device)
+        if quantize and scales is None:
+            scales = torch.empty((M, 1), dtype=torch.float32, device=r.device)
+        pn = _bytes8(n_out, "n_out") if quantize else _typed(n_out, "n_out", ndt, (M, K))
+        if tuple(n_out.shape) != (M, K):
+            raise ValueError(f"n_out must have shape {(M, K)}")
+        if not quantize and scales is not None:
+            raise ValueError("scales need quantize")
+        rc = load_library().residual_norm(
+            *args, _typed(r_out, "r_out", r.dtype, (M, K)), pn,
+            _f32(scales, "scales", (M,)) if quantize else None, M, K, _stream(stream))
+    _check("residual_norm", rc)
+    h = r if y is None else r_out
+    return (h, n_out, scales) if quantize else (h, n_out)
+
+
+def residual_norm_backward(y, r, w_pre, dn, dr_out=None, w_post=None, gate=None, alpha=1.0,
+                           beta=1.0, eps=1e-6, dy=None, dr=None, dw_pre=None, dw_post=None,
+                           dgate=None, workspace=None, stream=None):
+    """(dy, dr, dw_pre, dw_post, dgate) of residual_norm for dn bf16 [M][K]
+    and dr_out [M][K] of r's type (None: zero); the vector gradients fp32 [K].
+    None for what is not there."""
+    torch = _torch()
+    _ffn_device(stream, y=y, r=r, w_pre=w_pre, w_post=w_post, gate=gate, dn=dn, dr_out=dr_out,
+                dy=dy, dr=dr, dw_pre=dw_pre, dw_post=dw_post, dgate=dgate, workspace=workspace)
+    M, K, args = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps)
+    L = load_library()
+    bf, f32 = torch.bfloat16, torch.float32
+    with _on(stream):
+        if y is None:
+            if dy is not None:
+                raise ValueError("without y there is no dy")
+        elif dy is None:
+            dy = torch.empty_like(y)
+        if dr is None:
+            dr = torch.empty_like(r)
+        vectors = []
+        for name, w, dw in (("dw_post", w_post, dw_post), ("dgate", gate, dgate),
+                            ("dw_pre", w_pre, dw_pre)):
+            if w is None and dw is not None:
+                raise ValueError(f"{name} without its vector")
+            if w is not None and dw is None:
+                dw = torch.empty(K, dtype=f32, device=r.device)
+            vectors.append((_typed(dw, name, f32, (K,)), dw))
+        (p_post, dw_post), (p_gate, dgate), (p_pre, dw_pre) = vectors
+        need = L.qll_residual_norm_backward_workspace_bytes(M, K)
+        ws, wsb = _scratch("qll_residual_norm_backward_workspace_bytes", need, workspace, r.device)
+        rc = L.residual_norm_backward(
+            *args, _typed(dn, "dn", bf, (M, K)), _typed(dr_out, "dr_out", r.dtype, (M, K)),
+            _typed(dy, "dy", bf, (M, K)), _typed(dr, "dr", r.dtype, (M, K)), p_post,
+            p_gate, p_pre, M, K, _ptr(ws), wsb, _stream(stream))
+    _check("residual_norm_backward", rc)
+    return dy, dr, dw_pre, dw_post, dgate
 
 
 # --------------------------------------------------------------------------

@@ -1,0 +1,366 @@
+// Tiled matrix products of the feed-forward operators for gfx950.
+//
+//   out[r][c] = epilogue(sum_k Q[r][k] P[c][k])
+//
+// P is the operand along the output's columns and takes the row side of the
+// matrix cores, Q the one along its rows: a lane then holds 4 consecutive
+// output columns of one row per 16x16 block, and with the P rows of two
+// blocks interleaved by fours, 8 of them.  So outputs, residuals and biases
+// move as 8- or 16-byte vectors straight from the accumulators, with no trip
+// through LDS, and the gate and up sums of one output are in one lane.
+//
+// A tile is BP x BQ over WP x WQ waves; each operand's tile rows come in two
+// halves.  A stage is 128 bytes of a K-contiguous row (64 bf16 or 128 e4m3
+// elements).  LDS images of one half of H rows, H * 128 bytes either way:
+//   K-contiguous operand: [H][128 bytes], 16-byte chunks XOR-swizzled by row;
+//   K-strided operand (bf16): [64 k][H * 2 bytes], as it lies in memory; the
+//     fragments are read with ds_read_b64_tr_b16, which hands lane i of 16
+//     the i-th column of a 4 x 16 block.  32-byte pairs of chunks are
+//     XOR-swizzled by k so that the eight k lines that 32 lanes read at once
+//     fall on distinct banks.
+// Copies go from global memory to LDS directly (buffer_load_dwordx4 ... lds)
+// through resources that end where the matrix ends: rows past the end, and K
+// past the end of a strided operand, read as zeros; K past the end of a
+// contiguous row gets an offset out of range.  Resources are rebuilt per
+// stage from 64-bit addresses, so no operand size overflows 32-bit offsets.
+#pragma once
+
+#include "ffn_epilogue.h"
+#include "gemm_pipe.h"
+
+namespace qll {
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+// Bank swizzles (see the header comment).  NB: interleaved blocks per half.
+// P, contiguous: the 16 rows of a fragment are 4 NB a + 4 j + b (a, b < 4).
+template <int NB>
+__device__ __forceinline__ int ffn_swz(int row)
+{
+    return ((row & 3) | (((row / (4 * NB)) & 1) << 2)) ^ ((row / (8 * NB)) & 1);
+}
+// strided: 32-byte pair key of k line `k` for lines of H * 2 bytes
+template <int H>
+__device__ __forceinline__ int ffn_kkey(int k)
+{
+    if constexpr (H >= 128)
+        return (k & 3) | (((k >> 3) & 1) << 2);
+    else if constexpr (H == 64)
+        return ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+    else
+        return (k >> 3) & 1;
+}
+
+// One operand's geometry within a tile of B rows over W waves (WAVES in all):
+// STR strided, ILV the blocks of a half interleaved by fours.
+template <int B, int W, int WAVES, bool STR, bool ILV>
+struct FfnSide {
+    static constexpr int H = B / 2;               // rows of a half
+    static constexpr int HB = H * 128;            // its bytes in LDS
+    static constexpr int SH = H / W;              // a wave's rows of a half
+    static constexpr int NB = SH / 16;            // its 16-row blocks
+    static constexpr int LD = HB / 1024 / WAVES;  // copies per wave and half
+    static constexpr int NBI = ILV ? NB : 1;      // interleaved blocks
+    static constexpr int CPL = H / 8;             // strided: chunks per k line
+    static_assert(SH % 16 == 0 && HB % (1024 * WAVES) == 0 && H <= 128, "tile geometry");
+
+    // local row of fragment row i of block j, within the wave's share
+    static __device__ __forceinline__ int frag_row(int j, int i)
+    {
+        return ILV ? 4 * NB * (i >> 2) + 4 * j + (i & 3) : 16 * j + i;
+    }
+    // copy i of this wave: this lane's LDS line and logical 16-byte chunk
+    static __device__ __forceinline__ void source(int i, int wave, int lane, int& line, int& ch)
+    {
+        const int L = (i * WAVES + wave) * 64 + lane;
+        if constexpr (STR) {
+            line = L / CPL;
+            ch = (L % CPL) ^ (ffn_kkey<H>(line) << 1);
+        } else {
+            line = L / 8;
+            ch = (L % 8) ^ ffn_swz<NBI>(line);
+        }
+    }
+};
+
+// Row of the tile that local row r of half h stands for.  SPLIT: the halves
+// interleave per wave share (a wave's 2 SH rows are consecutive); else half h
+// is rows h * H .. of the tile.
+template <typename S, bool SPLIT>
+__device__ __forceinline__ int ffn_tile_row(int h, int r)
+{
+    return SPLIT ? (r / S::SH) * 2 * S::SH + h * S::SH + r % S::SH : h * S::H + r;
+}
+
+// Resource of `base` from byte `off` to byte `avail` (none left: reads zeros).
+__device__ __forceinline__ v4i ffn_rsrc(const uint8_t* base, int64_t off, int64_t avail)
+{
+    const int64_t left = avail - off;
+    return buffer_rsrc(base + (left > 0 ? off : 0),
+                       (uint32_t)(left <= 0 ? 0 : (left < 0x7FFFFFFF ? left : 0x7FFFFFFF)));
+}
+
+template <bool FP8>
+__device__ __forceinline__ v4f ffn_mfma(const uint4 (&p)[2], const uint4 (&q)[2], v4f c)
+{
+    if constexpr (FP8) {
+        return mfma_step<OP_FP8>(p, q, c);
+    } else {
+        c = mfma_step<OP_BF16>(&p[0], &q[0], c);
+        return mfma_step<OP_BF16>(&p[1], &q[1], c);
+    }
+}
+
+// Fragment (16 rows, one 128-byte stage: two 16-byte pieces per lane) of
+// block j of this wave's share of a half.  An e4m3 lane takes chunks g and
+// 4 + g of its row in both operands: a reordering of K within the
+// instruction's 128, the same on both sides.
+template <typename S, bool STR>
+__device__ __forceinline__ void ffn_frag(const uint8_t* half, int w, int j, int lane, uint4 (&f)[2])
+{
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (STR) {
+        const int pair = (w * S::SH) / 16 + j;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            v4s t[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = ks * 32 + g * 8 + s * 4 + (i >> 2);
+                const uint8_t* p = half + k * (S::H * 2) + ((pair ^ ffn_kkey<S::H>(k)) << 5) +
+                                   ((i & 3) << 3);
+                t[s] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) v4s*)p);
+            }
+            const uint2 lo = __builtin_bit_cast(uint2, t[0]), hi = __builtin_bit_cast(uint2, t[1]);
+            f[ks] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+    } else {
+        const int row = w * S::SH + S::frag_row(j, i);
+        const int key = ffn_swz<S::NBI>(row);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+            f[ks] = *(const uint4*)(half + row * 128 + (((ks * 4 + g) ^ key) << 4));
+    }
+}
+
+// The epilogue of one wave: acc[h][j][hq][i], see FfnSide for the rows.
+template <typename SP, typename SQ, bool DUAL, int EPI>
+__device__ __forceinline__ void ffn_finish(const FfnArgs& a, v4f (&acc)[2][SP::NB][2][SQ::NB],
+                                           int c0, int r0, int tile_r, int wp, int wq, int wqn,
+                                           int lane)
+{
+    // vectors of W consecutive columns (JV blocks), NV of them per half
+    constexpr int W = 4 * SP::NBI;
+    constexpr int JV = W / 4;
+    constexpr int NV = SP::NB / JV;
+    static_assert(SP::NBI <= 2, "interleave at most two blocks");
+    const int g = lane >> 4;
+    const bool vec = a.C % W == 0;
+    auto run = [&](auto A) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(A)::value;
+#pragma unroll
+        for (int h = 0; h < (DUAL ? 1 : 2); ++h)
+#pragma unroll
+            for (int jv = 0; jv < NV; ++jv) {
+                const int local = wp * SP::SH + SP::frag_row(jv * JV, 4 * g);
+                const int c = c0 + ffn_tile_row<SP, !DUAL>(h, local);
+                float cs[W];
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    cs[e] = 0.0f;
+#pragma unroll
+                for (int hq = 0; hq < 2; ++hq)
+#pragma unroll
+                    for (int i = 0; i < SQ::NB; ++i) {
+                        const int r = r0 + hq * SQ::H + wq * SQ::SH + 16 * i + (lane & 15);
+                        float v[W], u[W];
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            v[e] = acc[h][jv * JV + e / 4][hq][i][e & 3];
+                            u[e] = DUAL ? acc[1][jv * JV + e / 4][hq][i][e & 3] : 0.0f;
+                        }
+                        ffn_store_act<EPI, W, ACT>(a, v, u, r, c, vec, cs);
+                    }
+                if constexpr (EPI == EPI_DZ) {
+                    // the wave's column sums over its rows (16 lanes share a
+                    // column vector): one row of `partial` per tile and wave
+                    // row, added up in a fixed order by launch_colsum_finish
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+#pragma unroll
+                        for (int d = 1; d < 16; d <<= 1)
+                            cs[e] += __shfl_xor(cs[e], d, 64);
+                    if (a.partial && (lane & 15) == 0 && c < a.C)
+                        store_f32<W>(a.partial + (size_t)(tile_r * wqn + wq) * a.C + c, cs);
+                }
+            }
+    };
+    if constexpr (EPI == EPI_PARTIAL)
+        run(std::integral_constant<int, ACT_NONE>{});
+    else
+        with_act(a.act, run);
+}
+
+// A wave's copies of one tile: per-lane source offsets relative to the tile's
+// corner, and the copies of one half of one operand at stage kt.
+template <bool FP8, int LAY, bool DUAL, int BP, int BQ, int WP, int WQ>
+struct FfnCopies {
+    static constexpr int WAVES = WP * WQ;
+    static constexpr bool PSTR = LAY != LAY_NT, QSTR = LAY == LAY_TN;
+    static_assert(!FP8 || LAY == LAY_NT, "e4m3 operands are K-contiguous");
+    using SP = FfnSide<BP, WP, WAVES, PSTR, !PSTR>;
+    using SQ = FfnSide<BQ, WQ, WAVES, QSTR, false>;
+    static constexpr int SLOT = (BP + BQ) * 128;
+
+    const FfnArgs& a;
+    int c0, r0, wave;
+    uint32_t kbytes;
+    uint32_t vp[2][SP::LD], vq[2][SQ::LD];
+    int chp[SP::LD], chq[SQ::LD];
+
+    __device__ __forceinline__ FfnCopies(const FfnArgs& args, int c, int r, int w, int lane)
+        : a(args), c0(c), r0(r), wave(w), kbytes((uint32_t)args.klen * (FP8 ? 1 : 2))
+    {
+#pragma unroll
+        for (int i = 0; i < SP::LD; ++i) {
+            int line;
+            SP::source(i, wave, lane, line, chp[i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int hh = DUAL ? 0 : h;  // the two weights have a base each
+                vp[h][i] = PSTR ? (uint32_t)line * (uint32_t)a.ldp +
+                                      2 * ffn_tile_row<SP, !DUAL>(hh, chp[i] * 8)
+                                : (uint32_t)ffn_tile_row<SP, !DUAL>(hh, line) * (uint32_t)a.ldp +
+                                      chp[i] * 16;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SQ::LD; ++i) {
+            int line;
+            SQ::source(i, wave, lane, line, chq[i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                vq[h][i] = QSTR ? (uint32_t)line * (uint32_t)a.ldq +
+                                      2 * ffn_tile_row<SQ, false>(h, chq[i] * 8)
+                                : (uint32_t)ffn_tile_row<SQ, false>(h, line) * (uint32_t)a.ldq +
+                                      chq[i] * 16;
+        }
+    }
+    __device__ __forceinline__ void copy_p(int h, int kt, uint8_t* slot) const
+    {
+        const int seg = kt >= a.nks ? 1 : 0;
+        const int kk = kt - seg * a.nks;
+        const uint32_t kb = (uint32_t)kk * 128u;
+        const int src = DUAL ? h : seg;
+        const v4i rs = ffn_rsrc(a.P[src],
+                                PSTR ? (int64_t)kk * 64 * a.ldp + 2 * c0 : (int64_t)c0 * a.ldp + kb,
+                                a.availP[src]);
+#pragma unroll
+        for (int i = 0; i < SP::LD; ++i) {
+            uint32_t vo = vp[h][i];
+            if (!PSTR && kb + 128 > kbytes && kb + chp[i] * 16 >= kbytes)
+                vo = kOutOfRange;
+            dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+                              slot + h * SP::HB + (i * WAVES + wave) * 1024)));
+        }
+    }
+    __device__ __forceinline__ void copy_q(int h, int kt, uint8_t* slot) const
+    {
+        const int seg = kt >= a.nks ? 1 : 0;
+        const int kk = kt - seg * a.nks;
+        const uint32_t kb = (uint32_t)kk * 128u;
+        const v4i rs = ffn_rsrc(a.Q[seg],
+                                QSTR ? (int64_t)kk * 64 * a.ldq + 2 * r0 : (int64_t)r0 * a.ldq + kb,
+                                a.availQ[seg]);
+#pragma unroll
+        for (int i = 0; i < SQ::LD; ++i) {
+            uint32_t vo = vq[h][i];
+            if (!QSTR && kb + 128 > kbytes && kb + chq[i] * 16 >= kbytes)
+                vo = kOutOfRange;
+            dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+                              slot + 2 * SP::HB + h * SQ::HB + (i * WAVES + wave) * 1024)));
+        }
+    }
+};
+
+// Ring of S stages: every wave copies its share of stage kt + S - 1 while the
+// workgroup computes stage kt; one barrier per stage.
+template <bool FP8, int LAY, int EPI, int BP, int BQ, int WP, int WQ, int S>
+__global__ __launch_bounds__(WP* WQ * 64) void ffn_ring_kernel(FfnArgs a)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
+    using Copies = FfnCopies<FP8, LAY, DUAL, BP, BQ, WP, WQ>;
+    using SP = typename Copies::SP;
+    using SQ = typename Copies::SQ;
+    constexpr int SLOT = Copies::SLOT;
+    constexpr int LPT = 2 * (SP::LD + SQ::LD);  // copies per wave and stage
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * SLOT];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave % WP, wq = wave / WP;
+    constexpr int TC = DUAL ? BP / 2 : BP;  // output columns of a tile
+    const int tr = (a.R + BQ - 1) / BQ, tc = (a.C + TC - 1) / TC;
+    int tile_r, tile_c;
+    xcd_tile(blockIdx.x, tr, tc, 4, tile_r, tile_c);
+    const int r0 = tile_r * BQ, c0 = tile_c * TC;
+    const int kt0 = blockIdx.y * a.per;
+    const int kt1 = min(a.nseg * a.nks, kt0 + a.per);
+    const Copies cp(a, c0, r0, wave, lane);
+    auto issue = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
+        cp.copy_p(0, kt, slot);
+        cp.copy_p(1, kt, slot);
+        cp.copy_q(0, kt, slot);
+        cp.copy_q(1, kt, slot);
+    };
+
+    v4f acc[2][SP::NB][2][SQ::NB];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < SP::NB; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < SQ::NB; ++i)
+                    acc[h][j][q][i] = v4f{0, 0, 0, 0};
+
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+        if (kt0 + s < kt1)
+            issue(kt0 + s, ring + s * SLOT);
+    int slot = 0;
+    for (int kt = kt0; kt < kt1; ++kt) {
+        // stage kt has landed for every wave, and every wave is done reading
+        // the slot that the next copy overwrites
+        wait_younger<S - 2, LPT>(min(S - 2, kt1 - 1 - kt));
+        if (kt + S - 1 < kt1)
+            issue(kt + S - 1, ring + (slot == 0 ? S - 1 : slot - 1) * SLOT);
+        const uint8_t* sp = ring + slot * SLOT;
+        const uint8_t* sq = sp + 2 * SP::HB;
+        uint4 fp[2][SP::NB][2], fq[SQ::NB][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < SP::NB; ++j)
+                ffn_frag<SP, Copies::PSTR>(sp + h * SP::HB, wp, j, lane, fp[h][j]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 0; i < SQ::NB; ++i)
+                ffn_frag<SQ, Copies::QSTR>(sq + q * SQ::HB, wq, i, lane, fq[i]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < SP::NB; ++j)
+#pragma unroll
+                    for (int i = 0; i < SQ::NB; ++i)
+                        acc[h][j][q][i] = ffn_mfma<FP8>(fp[h][j], fq[i], acc[h][j][q][i]);
+        }
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    ffn_finish<SP, SQ, DUAL, EPI>(a, acc, c0, r0, tile_r, wp, wq, WQ, lane);
+}
+
+}  // namespace qll

@@ -1,0 +1,13 @@
+// bf16 products with two K-strided operands (gradient of the weights).
+#include "ffn_launch.h"
+
+namespace qll {
+
+hipError_t ffn_launch_tn(int tile, int epi, const FfnArgs& a, hipStream_t stream)
+{
+    if (epi == EPI_LINEAR)
+        return ffn_launch_tile<false, LAY_TN, EPI_LINEAR>(tile, a, stream);
+    return ffn_launch_tile<false, LAY_TN, EPI_PARTIAL>(tile, a, stream);
+}
+
+}  // namespace qll
