@@ -165,9 +165,15 @@ def _ensure_init():
 # marshalling helpers (plumbing only)
 # --------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t, name):
@@ -563,90 +569,141 @@ def grouped_select(M: int, E: int) -> str:
 # feed-forward operators
 # --------------------------------------------------------------------------
 
-def _ffn_device(stream, **tensors):
-    """The operators launch on the current device: every tensor (and the
-    stream, if given) has to be there."""
+# These calls take a few microseconds on the device, so the checks here are
+# written for speed: one pass per tensor, and no context manager when the call
+# runs on the current stream.  A call with `stream` makes it the current one
+# and calls itself, so that what it allocates belongs to that stream too.
+
+def _under(stream, fn, *args, **kw):
     torch = _torch()
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on the GPU")
-        if t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
-    if stream is not None and stream.device.index != here:
+    if stream.device.index != here:
         raise ValueError(f"stream is on {stream.device}, the current device is cuda:{here}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
-def _typed(t, name, dtype, shape):
-    """Pointer of a contiguous tensor of this type and shape, None for None."""
+def _place():
+    """(current device, its current stream's handle)"""
+    torch = _torch()
+    here = torch.cuda.current_device()
+    return here, torch._C._cuda_getCurrentRawStream(here)
+
+
+def _refuse(t, name, what, here):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {what}")
+
+
+def _arg(t, name, dtype, shape, here):
+    """Pointer of a contiguous tensor of this type and shape on the current
+    device; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return _dev_ptr(t, name)
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == here and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, f"{dtype} of shape {tuple(shape)}", here)
 
 
-def _act(act):
-    if act not in ACT:
-        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACT)}")
-    return ACT[act]
-
-
-def _float_out(out, M, N, out_dtype, device):
-    if out_dtype not in ("bf16", "fp32"):
-        raise ValueError("out_dtype must be 'bf16' or 'fp32'")
-    return _out(out, M, N, out_dtype, device)
-
-
-def _scratch(query, need, workspace, device):
-    """(workspace, bytes) of at least `need` bytes, allocated if not given."""
+def _codes(t, name, shape, here):
+    """Pointer of e4m3 codes: float8_e4m3fn, or their bytes."""
     torch = _torch()
-    if need < 0:
-        raise QllError(query, -need)
-    if need == 0:
-        return None, 0
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _dev_ptr(workspace, "workspace")
-    return workspace, workspace.numel() * workspace.element_size()
+    dt = getattr(t, "dtype", None)
+    if dt is torch.uint8 or dt is torch.int8:
+        return _arg(t, name, dt, shape, here)
+    return _arg(t, name, torch.float8_e4m3fn, shape, here)
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+def _scales(t, name, n, here):
+    """Pointer of n fp32 scales, [n] or [n][1]."""
+    shape = (n, 1) if getattr(t, "ndim", 1) == 2 else (n,)
+    return _arg(t, name, _torch().float32, shape, here)
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise TypeError(f"{name} must be a torch tensor")
 
 
 def _matrix(t, name):
-    if t.dim() != 2:
+    if getattr(t, "ndim", None) != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     return t.shape
 
 
-def _epilogue(fp8, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace, stream):
+def _act(act):
+    code = ACT.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACT)}")
+    return code
+
+
+def _float_out(out, M, N, out_dtype, like, here):
+    """(output, its pointer, its code), allocated if not given."""
     torch = _torch()
-    _ffn_device(stream, A=A, B=B, sa=sa, sb=sb, bias=bias, residual=residual, out=out,
-                workspace=workspace)
+    if out_dtype == "bf16":
+        dt, code = torch.bfloat16, 0
+    elif out_dtype == "fp32":
+        dt, code = torch.float32, 1
+    else:
+        raise ValueError("out_dtype must be 'bf16' or 'fp32'")
+    if out is None:
+        out = like.new_empty((M, N), dtype=dt)
+        return out, out.data_ptr(), code
+    return out, _arg(out, "out", dt, (M, N), here), code
+
+
+def _scratch(query, need, workspace, like, here):
+    """(pointer, bytes, tensor to keep) of at least `need` bytes, allocated if
+    not given."""
+    if need <= 0:
+        if need < 0:
+            raise QllError(query, -need)
+        return None, 0, None
+    torch = _torch()
+    if workspace is None:
+        workspace = like.new_empty(need, dtype=torch.uint8)
+    return (_arg(workspace, "workspace", workspace.dtype, workspace.shape, here),
+            workspace.numel() * workspace.element_size(), workspace)
+
+
+def _epilogue(fp8, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace):
+    torch = _torch()
+    here, st = _place()
+    _required(A=A, B=B)
     M, K = _matrix(A, "A")
-    N, K2 = _matrix(B, "B")
-    if K2 != K:
-        raise ValueError(f"A is [M][{K}] but B is [N][{K2}]")
-    code = _act(act)
-    L = load_library()
+    N = _matrix(B, "B")[0]
     bf = torch.bfloat16
-    args = ([_bytes8(A, "A"), _bytes8(B, "B"), _f32(sa, "sa", (M,)), _f32(sb, "sb", (N,))] if fp8
-            else [_typed(A, "A", bf, (M, K)), _typed(B, "B", bf, (N, K))])
-    args += [_typed(bias, "bias", bf, (N,)), _typed(residual, "residual", bf, (M, N)), code]
-    with _on(stream):
-        out = _float_out(out, M, N, out_dtype, A.device)
-        ws, wsb = _scratch("qll_epilogue_workspace_bytes",
-                           L.qll_epilogue_workspace_bytes(int(fp8), M, N, K), workspace, A.device)
-        fn = "gemm_fp8_epilogue" if fp8 else "gemm_bf16_epilogue"
-        rc = getattr(L, fn)(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K, _ptr(ws), wsb,
-                            _stream(stream))
-    _check(fn, rc)
+    L = load_library()
+    pb, pr = _arg(bias, "bias", bf, (N,), here), _arg(residual, "residual", bf, (M, N), here)
+    code = _act(act)
+    if fp8:
+        _required(sa=sa, sb=sb)
+        lead = (_codes(A, "A", (M, K), here), _codes(B, "B", (N, K), here),
+                _scales(sa, "sa", M, here), _scales(sb, "sb", N, here))
+        fn, f = "gemm_fp8_epilogue", L.gemm_fp8_epilogue
+    else:
+        lead = (_arg(A, "A", bf, (M, K), here), _arg(B, "B", bf, (N, K), here))
+        fn, f = "gemm_bf16_epilogue", L.gemm_bf16_epilogue
+    out, po, od = _float_out(out, M, N, out_dtype, A, here)
+    ws, wsb, keep = _scratch("qll_epilogue_workspace_bytes",
+                             L.qll_epilogue_workspace_bytes(fp8, M, N, K), workspace, A, here)
+    rc = f(*lead, pb, pr, code, po, od, M, N, K, ws, wsb, st)
+    if rc:
+        raise QllError(fn, rc)
     return out
 
 
@@ -654,14 +711,20 @@ def gemm_bf16_epilogue(A, B, bias=None, residual=None, act="none", out_dtype="bf
                        workspace=None, stream=None):
     """act(A B^T + bias) + residual: bf16 A [M][K], B [N][K], bias [N],
     residual [M][N]."""
-    return _epilogue(False, A, B, None, None, bias, residual, act, out_dtype, out, workspace, stream)
+    if stream is not None:
+        return _under(stream, gemm_bf16_epilogue, A, B, bias, residual, act, out_dtype, out,
+                      workspace)
+    return _epilogue(0, A, B, None, None, bias, residual, act, out_dtype, out, workspace)
 
 
 def gemm_fp8_epilogue(A, B, sa, sb, bias=None, residual=None, act="none", out_dtype="bf16",
                       out=None, workspace=None, stream=None):
     """act((A B^T) sa sb + bias) + residual: e4m3 A [M][K], B [N][K], fp32 sa
     [M], sb [N], bf16 bias [N], residual [M][N]."""
-    return _epilogue(True, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace, stream)
+    if stream is not None:
+        return _under(stream, gemm_fp8_epilogue, A, B, sa, sb, bias, residual, act, out_dtype, out,
+                      workspace)
+    return _epilogue(1, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace)
 
 
 def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=True,
@@ -670,74 +733,73 @@ def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=Tr
     """(dA, dB, dbias) of gemm_bf16_epilogue for bf16 dout [M][N] (the
     residual's gradient is dout itself): dA bf16 [M][K], dB bf16 [N][K], dbias
     fp32 [N]; None for what is not needed (dbias without a bias)."""
+    if stream is not None:
+        return _under(stream, gemm_bf16_epilogue_backward, A, B, dout, bias, act, need_input,
+                      need_weight, dA, dB, dbias, workspace)
     torch = _torch()
-    _ffn_device(stream, A=A, B=B, dout=dout, bias=bias, dA=dA, dB=dB, dbias=dbias,
-                workspace=workspace)
+    here, st = _place()
+    _required(A=A, B=B, dout=dout)
     M, K = _matrix(A, "A")
-    N, K2 = _matrix(B, "B")
-    if K2 != K:
-        raise ValueError(f"A is [M][{K}] but B is [N][{K2}]")
+    N = _matrix(B, "B")[0]
     code = _act(act)
     if not (need_input or need_weight or bias is not None):
         raise ValueError("nothing to compute")
     L = load_library()
     bf = torch.bfloat16
-    args = [_typed(A, "A", bf, (M, K)), _typed(B, "B", bf, (N, K)),
-            _typed(dout, "dout", bf, (M, N)), _typed(bias, "bias", bf, (N,)), code]
-    with _on(stream):
-        if need_input and dA is None:
-            dA = torch.empty_like(A)
-        if need_weight and dB is None:
-            dB = torch.empty_like(B)
-        if bias is not None and dbias is None:
-            dbias = torch.empty(N, dtype=torch.float32, device=A.device)
-        dA, dB = dA if need_input else None, dB if need_weight else None
-        dbias = dbias if bias is not None else None
-        need = L.qll_epilogue_backward_workspace_bytes(code, int(dbias is not None), M, N, K)
-        ws, wsb = _scratch("qll_epilogue_backward_workspace_bytes", need, workspace, A.device)
-        rc = L.gemm_bf16_epilogue_backward(
-            *args, _typed(dA, "dA", bf, (M, K)), _typed(dB, "dB", bf, (N, K)),
-            _typed(dbias, "dbias", torch.float32, (N,)), M, N, K, _ptr(ws), wsb, _stream(stream))
-    _check("gemm_bf16_epilogue_backward", rc)
+    pA, pB = _arg(A, "A", bf, (M, K), here), _arg(B, "B", bf, (N, K), here)
+    pd, pb = _arg(dout, "dout", bf, (M, N), here), _arg(bias, "bias", bf, (N,), here)
+    dA = (A.new_empty((M, K)) if dA is None else dA) if need_input else None
+    dB = (A.new_empty((N, K)) if dB is None else dB) if need_weight else None
+    if bias is None:
+        dbias = None
+    elif dbias is None:
+        dbias = A.new_empty(N, dtype=torch.float32)
+    ws, wsb, keep = _scratch(
+        "qll_epilogue_backward_workspace_bytes",
+        L.qll_epilogue_backward_workspace_bytes(code, bias is not None, M, N, K), workspace, A, here)
+    rc = L.gemm_bf16_epilogue_backward(
+        pA, pB, pd, pb, code, _arg(dA, "dA", bf, (M, K), here), _arg(dB, "dB", bf, (N, K), here),
+        _arg(dbias, "dbias", torch.float32, (N,), here), M, N, K, ws, wsb, st)
+    if rc:
+        raise QllError("gemm_bf16_epilogue_backward", rc)
     return dA, dB, dbias
-
-
-def _gated_sizes(A, Bg, Bu):
-    M, K = _matrix(A, "A")
-    N, K2 = _matrix(Bg, "Bg")
-    if K2 != K or tuple(Bu.shape) != (N, K):
-        raise ValueError(f"A is [M][{K}] but Bg is {tuple(Bg.shape)} and Bu {tuple(Bu.shape)}")
-    return M, N, K
 
 
 def gated_bf16(A, Bg, Bu, act="silu", out_dtype="bf16", out=None, stream=None):
     """act(A Bg^T) * (A Bu^T): bf16 A [M][K], Bg and Bu [N][K]."""
-    torch = _torch()
-    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, out=out)
-    M, N, K = _gated_sizes(A, Bg, Bu)
-    bf = torch.bfloat16
-    args = [_typed(A, "A", bf, (M, K)), _typed(Bg, "Bg", bf, (N, K)),
-            _typed(Bu, "Bu", bf, (N, K)), _act(act)]
-    with _on(stream):
-        out = _float_out(out, M, N, out_dtype, A.device)
-        rc = load_library().gated_bf16(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K,
-                                       _stream(stream))
-    _check("gated_bf16", rc)
+    if stream is not None:
+        return _under(stream, gated_bf16, A, Bg, Bu, act, out_dtype, out)
+    here, st = _place()
+    _required(A=A, Bg=Bg, Bu=Bu)
+    M, K = _matrix(A, "A")
+    N = _matrix(Bg, "Bg")[0]
+    bf = _torch().bfloat16
+    pA, pg = _arg(A, "A", bf, (M, K), here), _arg(Bg, "Bg", bf, (N, K), here)
+    pu = _arg(Bu, "Bu", bf, (N, K), here)
+    code = _act(act)
+    out, po, od = _float_out(out, M, N, out_dtype, A, here)
+    rc = load_library().gated_bf16(pA, pg, pu, code, po, od, M, N, K, st)
+    if rc:
+        raise QllError("gated_bf16", rc)
     return out
 
 
 def gated_fp8(A, Bg, Bu, sa, sg, su, act="silu", out_dtype="bf16", out=None, stream=None):
     """act((A Bg^T) sa sg) * ((A Bu^T) sa su): e4m3 A [M][K], Bg and Bu
     [N][K], fp32 sa [M], sg and su [N]."""
-    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, sa=sa, sg=sg, su=su, out=out)
-    M, N, K = _gated_sizes(A, Bg, Bu)
-    args = [_bytes8(A, "A"), _bytes8(Bg, "Bg"), _bytes8(Bu, "Bu"), _f32(sa, "sa", (M,)),
-            _f32(sg, "sg", (N,)), _f32(su, "su", (N,)), _act(act)]
-    with _on(stream):
-        out = _float_out(out, M, N, out_dtype, A.device)
-        rc = load_library().gated_fp8(*args, _dev_ptr(out, "out"), OUT[out_dtype], M, N, K,
-                                      _stream(stream))
-    _check("gated_fp8", rc)
+    if stream is not None:
+        return _under(stream, gated_fp8, A, Bg, Bu, sa, sg, su, act, out_dtype, out)
+    here, st = _place()
+    _required(A=A, Bg=Bg, Bu=Bu, sa=sa, sg=sg, su=su)
+    M, K = _matrix(A, "A")
+    N = _matrix(Bg, "Bg")[0]
+    lead = (_codes(A, "A", (M, K), here), _codes(Bg, "Bg", (N, K), here),
+            _codes(Bu, "Bu", (N, K), here), _scales(sa, "sa", M, here),
+            _scales(sg, "sg", N, here), _scales(su, "su", N, here), _act(act))
+    out, po, od = _float_out(out, M, N, out_dtype, A, here)
+    rc = load_library().gated_fp8(*lead, po, od, M, N, K, st)
+    if rc:
+        raise QllError("gated_fp8", rc)
     return out
 
 
@@ -745,40 +807,49 @@ def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weigh
                         dBg=None, dBu=None, workspace=None, stream=None):
     """(dA, dBg, dBu) of gated_bf16 for bf16 dout [M][N], all bf16; None for
     what is not needed."""
-    torch = _torch()
-    _ffn_device(stream, A=A, Bg=Bg, Bu=Bu, dout=dout, dA=dA, dBg=dBg, dBu=dBu, workspace=workspace)
-    M, N, K = _gated_sizes(A, Bg, Bu)
+    if stream is not None:
+        return _under(stream, gated_bf16_backward, A, Bg, Bu, dout, act, need_input, need_weight,
+                      dA, dBg, dBu, workspace)
+    here, st = _place()
+    _required(A=A, Bg=Bg, Bu=Bu, dout=dout)
+    M, K = _matrix(A, "A")
+    N = _matrix(Bg, "Bg")[0]
     if not (need_input or need_weight):
         raise ValueError("nothing to compute")
     L = load_library()
-    bf = torch.bfloat16
-    args = [_typed(A, "A", bf, (M, K)), _typed(Bg, "Bg", bf, (N, K)), _typed(Bu, "Bu", bf, (N, K)),
-            _typed(dout, "dout", bf, (M, N)), _act(act)]
-    with _on(stream):
-        dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
-        dBg = (torch.empty_like(Bg) if dBg is None else dBg) if need_weight else None
-        dBu = (torch.empty_like(Bu) if dBu is None else dBu) if need_weight else None
-        need = L.qll_gated_backward_workspace_bytes(M, N, K)
-        ws, wsb = _scratch("qll_gated_backward_workspace_bytes", need, workspace, A.device)
-        rc = L.gated_bf16_backward(
-            *args, _typed(dA, "dA", bf, (M, K)), _typed(dBg, "dBg", bf, (N, K)),
-            _typed(dBu, "dBu", bf, (N, K)), M, N, K, _ptr(ws), wsb, _stream(stream))
-    _check("gated_bf16_backward", rc)
+    bf = _torch().bfloat16
+    lead = (_arg(A, "A", bf, (M, K), here), _arg(Bg, "Bg", bf, (N, K), here),
+            _arg(Bu, "Bu", bf, (N, K), here), _arg(dout, "dout", bf, (M, N), here), _act(act))
+    dA = (A.new_empty((M, K)) if dA is None else dA) if need_input else None
+    dBg = (A.new_empty((N, K)) if dBg is None else dBg) if need_weight else None
+    dBu = (A.new_empty((N, K)) if dBu is None else dBu) if need_weight else None
+    ws, wsb, keep = _scratch("qll_gated_backward_workspace_bytes",
+                             L.qll_gated_backward_workspace_bytes(M, N, K), workspace, A, here)
+    rc = L.gated_bf16_backward(
+        *lead, _arg(dA, "dA", bf, (M, K), here), _arg(dBg, "dBg", bf, (N, K), here),
+        _arg(dBu, "dBu", bf, (N, K), here), M, N, K, ws, wsb, st)
+    if rc:
+        raise QllError("gated_bf16_backward", rc)
     return dA, dBg, dBu
 
 
-def _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps):
+def _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here):
     torch = _torch()
     bf = torch.bfloat16
+    _required(r=r, w_pre=w_pre)
     M, K = _matrix(r, "r")
-    if r.dtype not in (bf, torch.float32):
+    dt = r.dtype
+    if dt is bf:
+        kind = 0
+    elif dt is torch.float32:
+        kind = 1
+    else:
         raise ValueError("r must be bfloat16 or float32")
     if y is None and (w_post is not None or gate is not None or alpha != 1.0):
         raise ValueError("w_post, gate and alpha need a block output y")
-    kind = OUT["bf16"] if r.dtype == bf else OUT["fp32"]
-    return M, K, [_typed(y, "y", bf, (M, K)), _dev_ptr(r, "r"), kind,
-                  _typed(w_post, "w_post", bf, (K,)), _typed(gate, "gate", bf, (K,)),
-                  _typed(w_pre, "w_pre", bf, (K,)), alpha, beta, eps]
+    return M, K, dt, (_arg(y, "y", bf, (M, K), here), _arg(r, "r", dt, (M, K), here), kind,
+                      _arg(w_post, "w_post", bf, (K,), here), _arg(gate, "gate", bf, (K,), here),
+                      _arg(w_pre, "w_pre", bf, (K,), here), alpha, beta, eps)
 
 
 def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
@@ -787,30 +858,36 @@ def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=
     (w_post y / rms(y)), n = w_pre h / rms(h).  y bf16 [M][K] (None: h = r), r
     bf16 or fp32 [M][K], vectors bf16 [K].  Returns (h, n) with n bf16, or with
     quantize (h, e4m3 codes, fp32 scales [M][1]).  r_out may be r."""
+    if stream is not None:
+        return _under(stream, residual_norm, y, r, w_pre, w_post, gate, alpha, beta, eps, quantize,
+                      r_out, n_out, scales)
     torch = _torch()
-    _ffn_device(stream, y=y, r=r, w_pre=w_pre, w_post=w_post, gate=gate, r_out=r_out, n_out=n_out,
-                scales=scales)
-    M, K, args = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps)
-    with _on(stream):
-        if y is None:
-            if r_out is not None:
-                raise ValueError("without y the stream is r itself")
-        elif r_out is None:
-            r_out = torch.empty_like(r)
-        ndt = torch.float8_e4m3fn if quantize else torch.bfloat16
+    here, st = _place()
+    M, K, dt, lead = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here)
+    ph = None
+    if y is None:
+        if r_out is not None:
+            raise ValueError("without y the stream is r itself")
+    elif r_out is None:
+        r_out = torch.empty_like(r)
+        ph = r_out.data_ptr()
+    else:
+        ph = _arg(r_out, "r_out", dt, (M, K), here)
+    if quantize:
         if n_out is None:
-            n_out = torch.empty((M, K), dtype=ndt, device=r.device)
-        if quantize and scales is None:
-            scales = torch.empty((M, 1), dtype=torch.float32, device=r.device)
-        pn = _bytes8(n_out, "n_out") if quantize else _typed(n_out, "n_out", ndt, (M, K))
-        if tuple(n_out.shape) != (M, K):
-            raise ValueError(f"n_out must have shape {(M, K)}")
-        if not quantize and scales is not None:
+            n_out = r.new_empty((M, K), dtype=torch.float8_e4m3fn)
+        if scales is None:
+            scales = r.new_empty((M, 1), dtype=torch.float32)
+        pn, ps = _codes(n_out, "n_out", (M, K), here), _scales(scales, "scales", M, here)
+    else:
+        if scales is not None:
             raise ValueError("scales need quantize")
-        rc = load_library().residual_norm(
-            *args, _typed(r_out, "r_out", r.dtype, (M, K)), pn,
-            _f32(scales, "scales", (M,)) if quantize else None, M, K, _stream(stream))
-    _check("residual_norm", rc)
+        if n_out is None:
+            n_out = r.new_empty((M, K), dtype=torch.bfloat16)
+        pn, ps = _arg(n_out, "n_out", torch.bfloat16, (M, K), here), None
+    rc = load_library().residual_norm(*lead, ph, pn, ps, M, K, st)
+    if rc:
+        raise QllError("residual_norm", rc)
     h = r if y is None else r_out
     return (h, n_out, scales) if quantize else (h, n_out)
 
@@ -821,36 +898,40 @@ def residual_norm_backward(y, r, w_pre, dn, dr_out=None, w_post=None, gate=None,
     """(dy, dr, dw_pre, dw_post, dgate) of residual_norm for dn bf16 [M][K]
     and dr_out [M][K] of r's type (None: zero); the vector gradients fp32 [K].
     None for what is not there."""
+    if stream is not None:
+        return _under(stream, residual_norm_backward, y, r, w_pre, dn, dr_out, w_post, gate, alpha,
+                      beta, eps, dy, dr, dw_pre, dw_post, dgate, workspace)
     torch = _torch()
-    _ffn_device(stream, y=y, r=r, w_pre=w_pre, w_post=w_post, gate=gate, dn=dn, dr_out=dr_out,
-                dy=dy, dr=dr, dw_pre=dw_pre, dw_post=dw_post, dgate=dgate, workspace=workspace)
-    M, K, args = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps)
+    here, st = _place()
+    M, K, dt, lead = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here)
+    _required(dn=dn)
     L = load_library()
     bf, f32 = torch.bfloat16, torch.float32
-    with _on(stream):
-        if y is None:
-            if dy is not None:
-                raise ValueError("without y there is no dy")
-        elif dy is None:
-            dy = torch.empty_like(y)
-        if dr is None:
-            dr = torch.empty_like(r)
-        vectors = []
-        for name, w, dw in (("dw_post", w_post, dw_post), ("dgate", gate, dgate),
-                            ("dw_pre", w_pre, dw_pre)):
-            if w is None and dw is not None:
-                raise ValueError(f"{name} without its vector")
-            if w is not None and dw is None:
-                dw = torch.empty(K, dtype=f32, device=r.device)
-            vectors.append((_typed(dw, name, f32, (K,)), dw))
-        (p_post, dw_post), (p_gate, dgate), (p_pre, dw_pre) = vectors
-        need = L.qll_residual_norm_backward_workspace_bytes(M, K)
-        ws, wsb = _scratch("qll_residual_norm_backward_workspace_bytes", need, workspace, r.device)
-        rc = L.residual_norm_backward(
-            *args, _typed(dn, "dn", bf, (M, K)), _typed(dr_out, "dr_out", r.dtype, (M, K)),
-            _typed(dy, "dy", bf, (M, K)), _typed(dr, "dr", r.dtype, (M, K)), p_post,
-            p_gate, p_pre, M, K, _ptr(ws), wsb, _stream(stream))
-    _check("residual_norm_backward", rc)
+    if y is None:
+        if dy is not None:
+            raise ValueError("without y there is no dy")
+    elif dy is None:
+        dy = torch.empty_like(y)
+    if dr is None:
+        dr = torch.empty_like(r)
+    vectors = []
+    for name, w, dw in (("dw_post", w_post, dw_post), ("dgate", gate, dgate),
+                        ("dw_pre", w_pre, dw_pre)):
+        if w is None and dw is not None:
+            raise ValueError(f"{name} without its vector")
+        if w is not None and dw is None:
+            dw = r.new_empty(K, dtype=f32)
+        vectors.append(dw)
+    dw_post, dgate, dw_pre = vectors
+    ws, wsb, keep = _scratch("qll_residual_norm_backward_workspace_bytes",
+                             L.qll_residual_norm_backward_workspace_bytes(M, K), workspace, r, here)
+    rc = L.residual_norm_backward(
+        *lead, _arg(dn, "dn", bf, (M, K), here), _arg(dr_out, "dr_out", dt, (M, K), here),
+        _arg(dy, "dy", bf, (M, K), here), _arg(dr, "dr", dt, (M, K), here),
+        _arg(dw_post, "dw_post", f32, (K,), here), _arg(dgate, "dgate", f32, (K,), here),
+        _arg(dw_pre, "dw_pre", f32, (K,), here), M, K, ws, wsb, st)
+    if rc:
+        raise QllError("residual_norm_backward", rc)
     return dy, dr, dw_pre, dw_post, dgate
 
 

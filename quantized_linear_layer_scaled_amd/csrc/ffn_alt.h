@@ -1,0 +1,275 @@
+// The 256x256 tile of the feed-forward products: eight waves in two groups
+// that alternate between the matrix cores and everything else.
+//
+// Waves w and w + 4 share a SIMD.  Group 0 (waves 0-3) and group 1 (4-7) run
+// the same sequence of phases, one barrier apart: while one group's waves
+// issue matrix instructions (and, among them, copies), the other's read
+// fragments from LDS, and at the next barrier they trade places.  A phase is one quadrant
+// (P half x Q half) of the wave's 64 x 128 share over one stage, 16 bf16 (or
+// 8 e4m3) instructions, 256 cycles:
+//
+//   phase   fragments read      copy started (2 per wave)   product
+//   0       Q0                  P0 of stage k + 2           P0 x Q0
+//   1       P1                  Q0 of stage k + 2           P1 x Q0
+//   2       Q1                  P1 of stage k + 2           P0 x Q1
+//   3       P0 of stage k + 1   Q1 of stage k + 2           P1 x Q1
+//
+// The two LDS slots hold stages k and k + 1; a half of stage k is overwritten
+// one phase after it was read (every wave waits for its reads before the
+// barrier that ends a read segment, and both groups have passed one by the
+// time either starts the copy).  At the end of the read segment before the
+// one that reads a half, five younger copies of two instructions are in
+// flight: s_waitcnt vmcnt(10) before that segment's barrier.  So a copy has
+// about six phases (3000 cycles) to land.  Copies past the last
+// stage are started all the same, which keeps that count; they read in range
+// or zeros, into slots nobody reads, and the kernel waits for them at the end
+// of the tile.
+//
+// One workgroup per CU walks over tiles blockIdx.x, + gridDim.x, ... (a
+// multiple of 8 workgroups, so each keeps to its XCD's tiles).  The epilogue
+// uses no LDS, so the next tile's first two stages are copied while it runs.
+#pragma once
+
+#include "ffn_tile.h"
+
+namespace qll {
+
+// One operand's source of the copies of a tile: its resource and this lane's
+// offset at the stage being copied.  A K-contiguous operand keeps its resource
+// (the tile's rows) and moves the offset; past the end of K the offset is out
+// of range.  A K-strided one keeps the offset and moves the resource by 64 k
+// lines; it ends where the matrix does.  All of it is 32-bit arithmetic once
+// per stage, so that a copy is one addition and the load.
+template <bool STR>
+struct FfnSource {
+    v4i rs;
+    uint32_t v;
+    int lines;  // strided: k lines from the stage to the end of the matrix
+    int kleft;  // contiguous: bytes of K from the stage to the end
+
+    // tile corner at row (column) x0 of `extent`; ch: this lane's chunk
+    __device__ __forceinline__ void set(const uint8_t* base, uint32_t ld, int x0, int extent,
+                                        int klen, int esz, uint32_t v0, int ch)
+    {
+        v = v0;
+        if constexpr (STR) {
+            const uint64_t at = (uint64_t)(uintptr_t)base + 2 * (int64_t)x0;
+            rs.x = (int)(uint32_t)at;
+            rs.y = (int)(uint32_t)(at >> 32) & 0xFFFF;
+            rs.w = 0x00020000;
+            lines = klen;
+            limit(ld, x0);
+        } else {
+            // (offsets stay below 256 rows, a row past `extent` is out of range)
+            const int rows = min(extent - x0, 256);
+            rs = buffer_rsrc(base + (int64_t)x0 * ld, (uint32_t)rows * ld);
+            kleft = klen * esz;
+            clip(ch);
+        }
+    }
+    __device__ __forceinline__ void limit(uint32_t ld, int x0)
+    {
+        // (one stage reads 64 lines: the last of them may end the matrix)
+        const int n = max(min(lines, 64), 0) * (int)ld - 2 * x0;
+        rs.z = __builtin_amdgcn_readfirstlane(max(n, 0));
+    }
+    __device__ __forceinline__ void clip(int ch)
+    {
+        if (kleft < 128 && ch * 16 >= kleft)
+            v = kOutOfRange;
+    }
+    __device__ __forceinline__ void next(uint32_t ld, int x0, int ch)
+    {
+        if constexpr (STR) {
+            const uint64_t at = (((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x) + 64ull * ld;
+            rs.x = (int)(uint32_t)at;
+            rs.y = (int)(uint32_t)(at >> 32);
+            lines -= 64;
+            limit(ld, x0);
+        } else {
+            v += 128;
+            kleft -= 128;
+            clip(ch);
+        }
+    }
+};
+
+template <bool FP8, int LAY, int EPI>
+__global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
+    using Copies = FfnCopies<FP8, LAY, DUAL, 256, 256, 4, 2>;
+    using SP = typename Copies::SP;
+    using SQ = typename Copies::SQ;
+    constexpr bool PSTR = Copies::PSTR, QSTR = Copies::QSTR;
+    constexpr bool SEGS = LAY == LAY_NN;
+    constexpr int SLOT = Copies::SLOT;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * SLOT];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave & 3, wq = wave >> 2;  // (wq is the group)
+    constexpr int TC = DUAL ? 128 : 256;
+    const int tr = (a.R + 255) / 256, tc = (a.C + TC - 1) / TC;
+    const int nk = a.nseg * a.nks;
+    const Copies cp(a, wave, lane);
+    int c0, r0;  // corner of the tile whose copies are being started
+
+    v4f acc[2][SP::NB][2][SQ::NB];
+
+    // sources of the next copies
+    FfnSource<PSTR> src_p[DUAL ? 2 : 1];
+    FfnSource<QSTR> src_q;
+    const uint32_t ldp = (uint32_t)a.ldp, ldq = (uint32_t)a.ldq;
+    int kp = 0, kq = 0;
+    auto set_p = [&](int seg) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < (DUAL ? 2 : 1); ++h)
+            src_p[h].set(a.P[DUAL ? h : seg], ldp, c0, a.C, a.klen, FP8 ? 1 : 2, cp.vp, cp.chp);
+    };
+    auto set_q = [&](int seg) __attribute__((always_inline)) {
+        src_q.set(a.Q[seg], ldq, r0, a.R, a.klen, FP8 ? 1 : 2, cp.vq, cp.chq);
+    };
+    // (only the input gradient has a second segment)
+    auto next_p = [&]() __attribute__((always_inline)) {
+        if (SEGS && ++kp == a.nks) {
+            set_p(1);
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < (DUAL ? 2 : 1); ++h)
+            src_p[h].next(ldp, c0, cp.chp);
+    };
+    auto next_q = [&]() __attribute__((always_inline)) {
+        if (SEGS && ++kq == a.nks) {
+            set_q(1);
+            return;
+        }
+        src_q.next(ldq, r0, cp.chq);
+    };
+    // copy i (of 2) of a half
+    auto copy_p = [&](int h, int i, uint8_t* slot) __attribute__((always_inline)) {
+        dma16(src_p[DUAL ? h : 0].v + cp.shift_p(h, i), src_p[DUAL ? h : 0].rs,
+              __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+                  slot + h * SP::HB + (i * 8 + wave) * 1024)));
+    };
+    auto copy_q = [&](int h, int i, uint8_t* slot) __attribute__((always_inline)) {
+        dma16(src_q.v + cp.shift_q(h, i), src_q.rs,
+              __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+                  slot + 2 * SP::HB + h * SQ::HB + (i * 8 + wave) * 1024)));
+    };
+
+    uint4 fp[2][SP::NB][2], fq[SQ::NB][2];
+    auto read_p = [&](int h, const uint8_t* slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < SP::NB; ++j)
+            ffn_frag<SP, PSTR>(slot + h * SP::HB, wp, j, lane, fp[h][j]);
+    };
+    auto read_q = [&](int h, const uint8_t* slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < SQ::NB; ++i)
+            ffn_frag<SQ, QSTR>(slot + 2 * SP::HB + h * SQ::HB, wq, i, lane, fq[i]);
+    };
+    // ends a read segment: the wave's reads are back, the copies that the
+    // next segment reads have landed
+    auto end_read = [&]() __attribute__((always_inline)) {
+        wait_vm_barrier<10>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // a quadrant's products; the two copies copy(0), copy(1) go out among them
+    auto product = [&](int h, int q, auto&& copy) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < SP::NB; ++j)
+#pragma unroll
+            for (int i = 0; i < SQ::NB; ++i) {
+                acc[h][j][q][i] = ffn_mfma<FP8>(fp[h][j], fq[i], acc[h][j][q][i]);
+                const int n = j * SQ::NB + i;
+                __builtin_amdgcn_sched_barrier(0);
+                if (n == 1 || n == 4)
+                    copy(n == 1 ? 0 : 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto stage = [&](uint8_t* slot, uint8_t* other) __attribute__((always_inline)) {
+        read_q(0, slot);
+        end_read();
+        product(0, 0, [&](int i) __attribute__((always_inline)) { copy_p(0, i, slot); });
+        read_p(1, slot);
+        end_read();
+        product(1, 0, [&](int i) __attribute__((always_inline)) { copy_q(0, i, slot); });
+        read_q(1, slot);
+        end_read();
+        product(0, 1, [&](int i) __attribute__((always_inline)) { copy_p(1, i, slot); });
+        next_p();
+        read_p(0, other);
+        end_read();
+        product(1, 1, [&](int i) __attribute__((always_inline)) { copy_q(1, i, slot); });
+        next_q();
+    };
+
+    // the first two stages of tile t
+    auto start = [&](int t) __attribute__((always_inline)) {
+        int tile_r, tile_c;
+        xcd_tile(t, tr, tc, 4, tile_r, tile_c);
+        r0 = tile_r * 256;
+        c0 = tile_c * TC;
+        kp = kq = 0;
+        set_p(0);
+        set_q(0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint8_t* slot = ring + s * SLOT;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    copy_p(h, i, slot);
+                    copy_q(h, i, slot);
+                }
+            next_p();
+            next_q();
+        }
+    };
+
+    const int tiles = tr * tc;
+    start(blockIdx.x);
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int rt = r0, ct = c0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < SP::NB; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < SQ::NB; ++i)
+                        acc[h][j][q][i] = v4f{0, 0, 0, 0};
+        // the copies have landed, and so have the stores of the tile before
+        // (they share the counter)
+        wait_vm_barrier<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        read_p(0, ring);
+        end_read();
+        if (wq == 1)
+            asm volatile("s_barrier" ::: "memory");
+        for (int kt = 0; kt < nk; kt += 2) {
+            stage(ring, ring + SLOT);
+            if (kt + 1 < nk)
+                stage(ring + SLOT, ring);
+        }
+        if (wq == 0)
+            asm volatile("s_barrier" ::: "memory");
+        // Copies started past the last stage still write this LDS.  Then the
+        // next tile's first stages travel while this one's epilogue runs.
+        wait_vm_barrier<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + gridDim.x < tiles)
+            start(t + gridDim.x);
+        ffn_finish<SP, SQ, DUAL, EPI>(a, acc, ct, rt, rt / 256, wp, wq, 2, lane);
+    }
+}
+
+}  // namespace qll

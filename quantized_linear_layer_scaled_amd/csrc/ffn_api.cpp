@@ -187,7 +187,7 @@ hipError_t input_gradient(const void* dz, const void* B0, const void* B1, void* 
     a.partial = partial;
     a.out = dA;
     a.ldo = K;
-    return ffn_launch(0, LAY_NN, EPI_LINEAR, a, stream);
+    return ffn_launch(0, LAY_NN, EPI_PLAIN, a, stream);
 }
 
 // dB [width][K] = dz^T A; rows from row_split on go to dB1.
@@ -212,7 +212,7 @@ hipError_t weight_gradient(const void* dz, const void* A, void* dB0, void* dB1, 
     a.out2 = dB1;
     a.row_split = (int)row_split;
     a.ldo = K;
-    return ffn_launch(0, LAY_TN, EPI_LINEAR, a, stream);
+    return ffn_launch(0, LAY_TN, EPI_PLAIN, a, stream);
 }
 
 int validate_backward(int64_t M, int64_t N, int64_t K, int act)

@@ -4,7 +4,7 @@
 #pragma once
 
 #include "ffn_internal.h"
-#include "gemm_tile.h"
+#include "gemm_pipe.h"
 
 namespace qll {
 
@@ -104,11 +104,18 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float* f)
         f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-template <int W>
+// NT: a non-temporal store, for outputs that all compute units write at the
+// same time at the end of their tiles: plain ones wait, dirty, in L2 and slow
+// the next tile's first copies (forward products at M = 8192, N = 12288,
+// K = 4096: 1-7% less with NT).
+template <int W, bool NT = false>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float* f)
 {
     static_assert(W == 4 || W == 8, "vector width");
-    if constexpr (W == 8)
+    if constexpr (W == 8 && NT)
+        store16_stream(p, bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
+                       bf16x2_rne(f[6], f[7]));
+    else if constexpr (W == 8)
         *(uint4*)p = make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
                                 bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7]));
     else
@@ -149,50 +156,52 @@ __device__ __forceinline__ void store_value(const FfnArgs& a, float v, int r, in
         ((uint16_t*)base)[i] = bf16_one(v);
 }
 
-// The W output columns c .. c + W - 1 of row r, whose fp32 sums are v (gated:
-// the gate's, u the up projection's).  `vec`: rows are whole vectors of W
-// (C % W == 0), so the vector is in range as a whole and aligned; else each
-// element is checked.  EPI_DZ adds its outputs to cs.
-template <int EPI, int W, int ACT>
-__device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const float* u, int r,
-                                              int c, bool vec, float* cs)
+// The same columns where rows are not whole vectors (C % W != 0): element by
+// element.  EPI_DZ, EPI_DGATED and EPI_PLAIN take whole vectors only.
+template <int EPI, int W>
+__device__ __forceinline__ void ffn_store_ragged(const FfnArgs& a, const float* v, const float* u,
+                                                 int r, int c)
 {
     if (r >= a.R)
         return;
-    if (!vec) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int ci = c + i;
-            if (ci >= a.C)
-                continue;
-            if constexpr (EPI == EPI_PARTIAL) {
-                a.partial[((size_t)blockIdx.y * a.R + r) * a.C + ci] = v[i];
-            } else if constexpr (EPI == EPI_LINEAR) {
-                float z = v[i];
-                if (a.sq)
-                    z = z * a.sq[r] * a.sp[0][ci];
-                if (a.bias)
-                    z += bf16_value(a.bias[ci]);
-                z = act_value<ACT>(z);
-                if (a.res)
-                    z += bf16_value(a.res[(size_t)r * a.C + ci]);
-                store_value(a, z, r, ci);
-            } else if constexpr (EPI == EPI_GATED) {
-                float g = v[i], up = u[i];
-                if (a.sq) {
-                    g = g * a.sq[r] * a.sp[0][ci];
-                    up = up * a.sq[r] * a.sp[1][ci];
-                }
-                store_value(a, act_value<ACT>(g) * up, r, ci);
+    for (int i = 0; i < W; ++i) {
+        const int ci = c + i;
+        if (ci >= a.C)
+            continue;
+        if constexpr (EPI == EPI_PARTIAL) {
+            a.partial[((size_t)blockIdx.y * a.R + r) * a.C + ci] = v[i];
+        } else if constexpr (EPI == EPI_LINEAR) {
+            store_value(a, linear_value(a, v[i], r, ci), r, ci);
+        } else if constexpr (EPI == EPI_GATED) {
+            float g = v[i], up = u[i];
+            if (a.sq) {
+                g = g * a.sq[r] * a.sp[0][ci];
+                up = up * a.sq[r] * a.sp[1][ci];
             }
-            // EPI_DZ and EPI_DGATED take whole vectors only
+            with_act(a.act, [&](auto A) { g = act_value<decltype(A)::value>(g); });
+            store_value(a, g * up, r, ci);
         }
-        return;
     }
+}
+
+// The W output columns c .. c + W - 1 of row r, whose fp32 sums are v (gated:
+// the gate's, u the up projection's); rows are whole vectors (C % W == 0), so
+// the vector is in range as a whole and aligned.  EPI_DZ adds its outputs to
+// cs.
+template <int EPI, int W, int ACT>
+__device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const float* u, int r,
+                                              int c, float* cs)
+{
+    if (r >= a.R)
+        return;
     if (c >= a.C)
         return;
     if constexpr (EPI == EPI_PARTIAL) {
         store_f32<W>(a.partial + ((size_t)blockIdx.y * a.R + r) * a.C + c, v);
+    } else if constexpr (EPI == EPI_PLAIN) {
+        uint16_t* base = (uint16_t*)(r < a.row_split ? a.out : a.out2);
+        store_bf16<W>(base + (size_t)(r < a.row_split ? r : r - a.row_split) * a.ldo + c, v);
     } else if constexpr (EPI == EPI_LINEAR) {
         if (a.sq) {
             const float s = a.sq[r];
@@ -222,7 +231,7 @@ __device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const 
         if (a.out_fp32)
             store_f32<W>((float*)base + at, v);
         else
-            store_bf16<W>((uint16_t*)base + at, v);
+            store_bf16<W, true>((uint16_t*)base + at, v);
     } else if constexpr (EPI == EPI_GATED) {
         float o[W];
         const float s = a.sq ? a.sq[r] : 1.0f;
@@ -238,7 +247,7 @@ __device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const 
         if (a.out_fp32)
             store_f32<W>((float*)a.out + (size_t)r * a.ldo + c, o);
         else
-            store_bf16<W>((uint16_t*)a.out + (size_t)r * a.ldo + c, o);
+            store_bf16<W, true>((uint16_t*)a.out + (size_t)r * a.ldo + c, o);
     } else if constexpr (EPI == EPI_DZ) {
         float b[W], d[W];
         load_bf16<W>(a.dy + (size_t)r * a.C + c, d);

@@ -18,6 +18,7 @@ enum FfnEpi : int {
     EPI_GATED,       // out = act(g) * u
     EPI_DZ,          // out = dy * act'(sum + bias[c]), column sums of out to `partial`
     EPI_DGATED,      // out[r][c] = dy * u * act'(g), out[r][C + c] = dy * act(g)
+    EPI_PLAIN,       // out = sum (rows from row_split on to out2)
     EPI_PARTIAL      // Split-K: fp32 sums to `partial` [split][R][C]
 };
 
@@ -72,7 +73,7 @@ hipError_t ffn_launch(int fp8, int layout, int epi, FfnArgs a, hipStream_t strea
 hipError_t ffn_launch_reduce(const FfnArgs& a, hipStream_t stream);
 // Few rows (R <= kFfnSkinnyRows): one pass over the weights, K split over the
 // waves of a workgroup.  EPI_LINEAR or EPI_GATED, both operands K-contiguous.
-constexpr int kFfnSkinnyRows = 64;
+constexpr int kFfnSkinnyRows = 16;
 hipError_t ffn_launch_skinny(int fp8, int epi, const FfnArgs& a, hipStream_t stream);
 
 // Column sums of bf16 x [R][C] over strips of kColsumRows rows -> fp32

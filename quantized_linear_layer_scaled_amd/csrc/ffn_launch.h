@@ -1,7 +1,7 @@
 // Tile shapes of the feed-forward products and the rule that picks one.
 #pragma once
 
-#include "ffn_tile.h"
+#include "ffn_alt.h"
 
 namespace qll {
 
@@ -18,9 +18,15 @@ hipError_t ffn_launch_tile(int tile, const FfnArgs& a, hipStream_t stream)
     const int B = kFfnTile[tile];
     const int64_t tiles = (int64_t)((a.R + B - 1) / B) * ((a.C + (DUAL ? B / 2 : B) - 1) / (DUAL ? B / 2 : B));
     const dim3 grid((unsigned)tiles, (unsigned)a.splits);
-    if (tile == 0)
-        ffn_ring_kernel<FP8, LAY, EPI, 256, 256, 4, 2, 2><<<grid, 512, 0, stream>>>(a);
-    else if (tile == 1)
+    if constexpr (EPI != EPI_PARTIAL) {  // (only the smallest tile splits K)
+        if (tile == 0) {
+            // one workgroup per CU
+            ffn_alt_kernel<FP8, LAY, EPI>
+                <<<(unsigned)(tiles < 256 ? tiles : 256), 512, 0, stream>>>(a);
+            return hipGetLastError();
+        }
+    }
+    if (tile == 1)
         ffn_ring_kernel<FP8, LAY, EPI, 128, 128, 2, 2, 2><<<grid, 256, 0, stream>>>(a);
     else
         ffn_ring_kernel<FP8, LAY, EPI, 64, 64, 2, 2, 4><<<grid, 256, 0, stream>>>(a);

@@ -5,8 +5,8 @@ namespace qll {
 
 hipError_t ffn_launch_nn(int tile, int epi, const FfnArgs& a, hipStream_t stream)
 {
-    if (epi == EPI_LINEAR)
-        return ffn_launch_tile<false, LAY_NN, EPI_LINEAR>(tile, a, stream);
+    if (epi == EPI_PLAIN)
+        return ffn_launch_tile<false, LAY_NN, EPI_PLAIN>(tile, a, stream);
     return ffn_launch_tile<false, LAY_NN, EPI_PARTIAL>(tile, a, stream);
 }
 

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnArgs a)
             v[3] += p.w;
         }
         with_act(a.act, [&](auto A) {
-            ffn_store_act<EPI_LINEAR, 4, decltype(A)::value>(a, v, nullptr, r, c, true, nullptr);
+            ffn_store_act<EPI_LINEAR, 4, decltype(A)::value>(a, v, nullptr, r, c, nullptr);
         });
     } else {
         float v = 0.0f;

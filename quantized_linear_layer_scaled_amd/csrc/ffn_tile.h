@@ -18,6 +18,12 @@
 //     the i-th column of a 4 x 16 block.  32-byte pairs of chunks are
 //     XOR-swizzled by k so that the eight k lines that 32 lanes read at once
 //     fall on distinct banks.
+// Lane group g = lane / 16 takes the 16-byte chunks 2 g and 2 g + 1 of a
+// stage (K elements 16 g .. 16 g + 15 of 64 in bf16): a reordering of K that
+// both operands share.  The LDS serves a b128 read 16 lanes at a time, from
+// two neighbouring groups; chunks g and g + 4 instead, with the same swizzle,
+// cost two passes for each (counters: 4 conflict cycles on 4 per read; none
+// this way).
 // Copies go from global memory to LDS directly (buffer_load_dwordx4 ... lds)
 // through resources that end where the matrix ends: rows past the end, and K
 // past the end of a strided operand, read as zeros; K past the end of a
@@ -44,11 +50,11 @@ template <int H>
 __device__ __forceinline__ int ffn_kkey(int k)
 {
     if constexpr (H >= 128)
-        return (k & 3) | (((k >> 3) & 1) << 2);
+        return (k & 3) | (((k >> 4) & 1) << 2);
     else if constexpr (H == 64)
-        return ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+        return ((k >> 1) & 1) | (((k >> 4) & 1) << 1);
     else
-        return (k >> 3) & 1;
+        return (k >> 4) & 1;
 }
 
 // One operand's geometry within a tile of B rows over W waves (WAVES in all):
@@ -112,9 +118,7 @@ __device__ __forceinline__ v4f ffn_mfma(const uint4 (&p)[2], const uint4 (&q)[2]
 }
 
 // Fragment (16 rows, one 128-byte stage: two 16-byte pieces per lane) of
-// block j of this wave's share of a half.  An e4m3 lane takes chunks g and
-// 4 + g of its row in both operands: a reordering of K within the
-// instruction's 128, the same on both sides.
+// block j of this wave's share of a half.
 template <typename S, bool STR>
 __device__ __forceinline__ void ffn_frag(const uint8_t* half, int w, int j, int lane, uint4 (&f)[2])
 {
@@ -126,7 +130,7 @@ __device__ __forceinline__ void ffn_frag(const uint8_t* half, int w, int j, int 
             v4s t[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k = ks * 32 + g * 8 + s * 4 + (i >> 2);
+                const int k = g * 16 + ks * 8 + s * 4 + (i >> 2);
                 const uint8_t* p = half + k * (S::H * 2) + ((pair ^ ffn_kkey<S::H>(k)) << 5) +
                                    ((i & 3) << 3);
                 t[s] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -140,7 +144,7 @@ __device__ __forceinline__ void ffn_frag(const uint8_t* half, int w, int j, int 
         const int key = ffn_swz<S::NBI>(row);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-            f[ks] = *(const uint4*)(half + row * 128 + (((ks * 4 + g) ^ key) << 4));
+            f[ks] = *(const uint4*)(half + row * 128 + (((2 * g + ks) ^ key) << 4));
     }
 }
 
@@ -155,48 +159,72 @@ __device__ __forceinline__ void ffn_finish(const FfnArgs& a, v4f (&acc)[2][SP::N
     constexpr int JV = W / 4;
     constexpr int NV = SP::NB / JV;
     static_assert(SP::NBI <= 2, "interleave at most two blocks");
+    // (opaque, so that a loop over tiles does not keep what is derived from
+    // it in registers through the products)
+    asm volatile("" : "+v"(lane));
     const int g = lane >> 4;
-    const bool vec = a.C % W == 0;
-    auto run = [&](auto A) __attribute__((always_inline)) {
-        constexpr int ACT = decltype(A)::value;
+    // f(h, jv, first column): the wave's column vectors
+    auto columns = [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < (DUAL ? 1 : 2); ++h)
 #pragma unroll
             for (int jv = 0; jv < NV; ++jv) {
                 const int local = wp * SP::SH + SP::frag_row(jv * JV, 4 * g);
-                const int c = c0 + ffn_tile_row<SP, !DUAL>(h, local);
-                float cs[W];
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    cs[e] = 0.0f;
-#pragma unroll
-                for (int hq = 0; hq < 2; ++hq)
-#pragma unroll
-                    for (int i = 0; i < SQ::NB; ++i) {
-                        const int r = r0 + hq * SQ::H + wq * SQ::SH + 16 * i + (lane & 15);
-                        float v[W], u[W];
-#pragma unroll
-                        for (int e = 0; e < W; ++e) {
-                            v[e] = acc[h][jv * JV + e / 4][hq][i][e & 3];
-                            u[e] = DUAL ? acc[1][jv * JV + e / 4][hq][i][e & 3] : 0.0f;
-                        }
-                        ffn_store_act<EPI, W, ACT>(a, v, u, r, c, vec, cs);
-                    }
-                if constexpr (EPI == EPI_DZ) {
-                    // the wave's column sums over its rows (16 lanes share a
-                    // column vector): one row of `partial` per tile and wave
-                    // row, added up in a fixed order by launch_colsum_finish
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-#pragma unroll
-                        for (int d = 1; d < 16; d <<= 1)
-                            cs[e] += __shfl_xor(cs[e], d, 64);
-                    if (a.partial && (lane & 15) == 0 && c < a.C)
-                        store_f32<W>(a.partial + (size_t)(tile_r * wqn + wq) * a.C + c, cs);
-                }
+                f(h, jv, c0 + ffn_tile_row<SP, !DUAL>(h, local));
             }
     };
-    if constexpr (EPI == EPI_PARTIAL)
+    // f(v, u, row): the sums of one column vector, row by row
+    auto rows = [&](int h, int jv, auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int hq = 0; hq < 2; ++hq) {
+            // (a limit on how many rows' loads are in registers)
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < SQ::NB; ++i) {
+                float v[W], u[W];
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    v[e] = acc[h][jv * JV + e / 4][hq][i][e & 3];
+                    u[e] = DUAL ? acc[1][jv * JV + e / 4][hq][i][e & 3] : 0.0f;
+                }
+                f(v, u, r0 + hq * SQ::H + wq * SQ::SH + 16 * i + (lane & 15));
+            }
+        }
+    };
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_PARTIAL) {
+        if (a.C % W != 0) {
+            columns([&](int h, int jv, int c) __attribute__((always_inline)) {
+                rows(h, jv, [&](float* v, float* u, int r) __attribute__((always_inline)) {
+                    ffn_store_ragged<EPI, W>(a, v, u, r, c);
+                });
+            });
+            return;
+        }
+    }
+    auto run = [&](auto A) __attribute__((always_inline)) {
+        columns([&](int h, int jv, int c) __attribute__((always_inline)) {
+            float cs[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                cs[e] = 0.0f;
+            rows(h, jv, [&](float* v, float* u, int r) __attribute__((always_inline)) {
+                ffn_store_act<EPI, W, decltype(A)::value>(a, v, u, r, c, cs);
+            });
+            if constexpr (EPI == EPI_DZ) {
+                // the wave's column sums over its rows (16 lanes share a
+                // column vector): one row of `partial` per tile and wave
+                // row, added up in a fixed order by launch_colsum_finish
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+#pragma unroll
+                    for (int d = 1; d < 16; d <<= 1)
+                        cs[e] += __shfl_xor(cs[e], d, 64);
+                if (a.partial && (lane & 15) == 0 && c < a.C)
+                    store_f32<W>(a.partial + (size_t)(tile_r * wqn + wq) * a.C + c, cs);
+            }
+        });
+    };
+    if constexpr (EPI == EPI_PARTIAL || EPI == EPI_PLAIN)
         run(std::integral_constant<int, ACT_NONE>{});
     else
         with_act(a.act, run);
@@ -214,40 +242,41 @@ struct FfnCopies {
     static constexpr int SLOT = (BP + BQ) * 128;
 
     const FfnArgs& a;
-    int c0, r0, wave;
+    int wave;
     uint32_t kbytes;
-    uint32_t vp[2][SP::LD], vq[2][SQ::LD];
-    int chp[SP::LD], chq[SQ::LD];
+    // the source offsets of copy 0 of half 0; the others differ by the same
+    // scalar in every lane
+    uint32_t vp, vq;
+    int chp, chq;
+    static constexpr int LINES_P = PSTR ? WAVES * 64 / SP::CPL : WAVES * 8;
+    static constexpr int LINES_Q = QSTR ? WAVES * 64 / SQ::CPL : WAVES * 8;
+    static_assert((PSTR || LINES_P % SP::SH == 0) && LINES_P % 32 == 0 && LINES_Q % 32 == 0,
+                  "copies of a half repeat the swizzle");
 
-    __device__ __forceinline__ FfnCopies(const FfnArgs& args, int c, int r, int w, int lane)
-        : a(args), c0(c), r0(r), wave(w), kbytes((uint32_t)args.klen * (FP8 ? 1 : 2))
+    __device__ __forceinline__ FfnCopies(const FfnArgs& args, int w, int lane)
+        : a(args), wave(w), kbytes((uint32_t)args.klen * (FP8 ? 1 : 2))
     {
-#pragma unroll
-        for (int i = 0; i < SP::LD; ++i) {
-            int line;
-            SP::source(i, wave, lane, line, chp[i]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int hh = DUAL ? 0 : h;  // the two weights have a base each
-                vp[h][i] = PSTR ? (uint32_t)line * (uint32_t)a.ldp +
-                                      2 * ffn_tile_row<SP, !DUAL>(hh, chp[i] * 8)
-                                : (uint32_t)ffn_tile_row<SP, !DUAL>(hh, line) * (uint32_t)a.ldp +
-                                      chp[i] * 16;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < SQ::LD; ++i) {
-            int line;
-            SQ::source(i, wave, lane, line, chq[i]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                vq[h][i] = QSTR ? (uint32_t)line * (uint32_t)a.ldq +
-                                      2 * ffn_tile_row<SQ, false>(h, chq[i] * 8)
-                                : (uint32_t)ffn_tile_row<SQ, false>(h, line) * (uint32_t)a.ldq +
-                                      chq[i] * 16;
-        }
+        int line;
+        SP::source(0, wave, lane, line, chp);
+        vp = PSTR ? (uint32_t)line * (uint32_t)a.ldp + 2 * ffn_tile_row<SP, !DUAL>(0, chp * 8)
+                  : (uint32_t)ffn_tile_row<SP, !DUAL>(0, line) * (uint32_t)a.ldp + chp * 16;
+        SQ::source(0, wave, lane, line, chq);
+        vq = QSTR ? (uint32_t)line * (uint32_t)a.ldq + 2 * ffn_tile_row<SQ, false>(0, chq * 8)
+                  : (uint32_t)ffn_tile_row<SQ, false>(0, line) * (uint32_t)a.ldq + chq * 16;
     }
-    __device__ __forceinline__ void copy_p(int h, int kt, uint8_t* slot) const
+    // what copy i of half h adds (DUAL: the two weights have a base each)
+    __device__ __forceinline__ uint32_t shift_p(int h, int i) const
+    {
+        const int hh = DUAL ? 0 : h;
+        return PSTR ? (uint32_t)(i * LINES_P) * (uint32_t)a.ldp + 2 * ffn_tile_row<SP, !DUAL>(hh, 0)
+                    : (uint32_t)ffn_tile_row<SP, !DUAL>(hh, i * LINES_P) * (uint32_t)a.ldp;
+    }
+    __device__ __forceinline__ uint32_t shift_q(int h, int i) const
+    {
+        return QSTR ? (uint32_t)(i * LINES_Q) * (uint32_t)a.ldq + 2 * ffn_tile_row<SQ, false>(h, 0)
+                    : (uint32_t)ffn_tile_row<SQ, false>(h, i * LINES_Q) * (uint32_t)a.ldq;
+    }
+    __device__ __forceinline__ void copy_p(int h, int kt, int c0, uint8_t* slot) const
     {
         const int seg = kt >= a.nks ? 1 : 0;
         const int kk = kt - seg * a.nks;
@@ -258,14 +287,14 @@ struct FfnCopies {
                                 a.availP[src]);
 #pragma unroll
         for (int i = 0; i < SP::LD; ++i) {
-            uint32_t vo = vp[h][i];
-            if (!PSTR && kb + 128 > kbytes && kb + chp[i] * 16 >= kbytes)
+            uint32_t vo = vp + shift_p(h, i);
+            if (!PSTR && kb + 128 > kbytes && kb + chp * 16 >= kbytes)
                 vo = kOutOfRange;
             dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
                               slot + h * SP::HB + (i * WAVES + wave) * 1024)));
         }
     }
-    __device__ __forceinline__ void copy_q(int h, int kt, uint8_t* slot) const
+    __device__ __forceinline__ void copy_q(int h, int kt, int r0, uint8_t* slot) const
     {
         const int seg = kt >= a.nks ? 1 : 0;
         const int kk = kt - seg * a.nks;
@@ -275,8 +304,8 @@ struct FfnCopies {
                                 a.availQ[seg]);
 #pragma unroll
         for (int i = 0; i < SQ::LD; ++i) {
-            uint32_t vo = vq[h][i];
-            if (!QSTR && kb + 128 > kbytes && kb + chq[i] * 16 >= kbytes)
+            uint32_t vo = vq + shift_q(h, i);
+            if (!QSTR && kb + 128 > kbytes && kb + chq * 16 >= kbytes)
                 vo = kOutOfRange;
             dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
                               slot + 2 * SP::HB + h * SQ::HB + (i * WAVES + wave) * 1024)));
@@ -307,12 +336,12 @@ __global__ __launch_bounds__(WP* WQ * 64) void ffn_ring_kernel(FfnArgs a)
     const int r0 = tile_r * BQ, c0 = tile_c * TC;
     const int kt0 = blockIdx.y * a.per;
     const int kt1 = min(a.nseg * a.nks, kt0 + a.per);
-    const Copies cp(a, c0, r0, wave, lane);
+    const Copies cp(a, wave, lane);
     auto issue = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
-        cp.copy_p(0, kt, slot);
-        cp.copy_p(1, kt, slot);
-        cp.copy_q(0, kt, slot);
-        cp.copy_q(1, kt, slot);
+        cp.copy_p(0, kt, c0, slot);
+        cp.copy_p(1, kt, c0, slot);
+        cp.copy_q(0, kt, r0, slot);
+        cp.copy_q(1, kt, r0, slot);
     };
 
     v4f acc[2][SP::NB][2][SQ::NB];

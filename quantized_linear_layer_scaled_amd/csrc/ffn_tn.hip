@@ -5,8 +5,8 @@ namespace qll {
 
 hipError_t ffn_launch_tn(int tile, int epi, const FfnArgs& a, hipStream_t stream)
 {
-    if (epi == EPI_LINEAR)
-        return ffn_launch_tile<false, LAY_TN, EPI_LINEAR>(tile, a, stream);
+    if (epi == EPI_PLAIN)
+        return ffn_launch_tile<false, LAY_TN, EPI_PLAIN>(tile, a, stream);
     return ffn_launch_tile<false, LAY_TN, EPI_PARTIAL>(tile, a, stream);
 }
 

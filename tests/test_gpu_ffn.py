@@ -56,7 +56,9 @@ def check(y, want, what, whole=None):
 # column, less than a vector, odd, ragged tiles; K: one chunk, ragged stages
 SIZES = [(1, 64, 128), (1, 1, 16), (3, 9, 48), (16, 129, 272), (17, 40, 1040), (33, 257, 528),
          (64, 520, 1056), (65, 64, 128), (65, 7, 32), (100, 333, 1040), (129, 130, 64), (200, 1000, 4112),
-         (257, 264, 656), (300, 2056, 400), (1025, 1041, 144)]
+         (257, 264, 656), (300, 2056, 400), (1025, 1041, 144),
+         # the 256x256 tile: one, two and several stages, ragged
+         (4100, 4360, 80), (4097, 4105, 208), (4200, 4104, 1040)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -99,7 +101,9 @@ def test_gated(qll, kind, M, N, K):
 
 
 GRAD_SIZES = [(1, 64, 128), (1, 8, 8), (5, 24, 40), (64, 72, 136), (65, 136, 72), (130, 264, 520),
-              (257, 520, 264), (300, 1032, 512), (1025, 264, 136), (2100, 1304, 264), (4096, 64, 64)]
+              (257, 520, 264), (300, 1032, 512), (1025, 264, 136), (2100, 1304, 264), (4096, 64, 64),
+              # the 256x256 tile in one of the products each
+              (4100, 72, 4360), (72, 4104, 4360), (4100, 4360, 72), (4100, 4360, 200)]
 
 
 @pytest.mark.parametrize("M,N,K", GRAD_SIZES)
