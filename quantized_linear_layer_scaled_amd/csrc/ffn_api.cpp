@@ -456,7 +456,7 @@ int64_t qll_residual_norm_backward_workspace_bytes(int64_t M, int64_t K)
         return -QLL_ERR_INVALID_ARG;
     if (K > kNormMaxK)
         return -QLL_ERR_UNSUPPORTED;
-    return (int64_t)3 * norm_backward_blocks(M, K) * K * 4;
+    return ((int64_t)3 * norm_backward_blocks(M, K) * K + norm_backward_stats(M, K)) * 4;
 }
 
 int residual_norm_backward(const void* y, const void* r, int r_dtype, const void* w_post,
@@ -478,7 +478,7 @@ int residual_norm_backward(const void* y, const void* r, int r_dtype, const void
         return QLL_ERR_MISALIGNED;
     const int blocks = norm_backward_blocks(M, K);
     if (M > 0) {
-        if (!ws || ws_bytes < (uint64_t)3 * blocks * K * 4)
+        if (!ws || ws_bytes < ((uint64_t)3 * blocks * K + norm_backward_stats(M, K)) * 4)
             return QLL_ERR_WORKSPACE;
         if (misaligned(ws, 16))
             return QLL_ERR_MISALIGNED;
@@ -489,6 +489,7 @@ int residual_norm_backward(const void* y, const void* r, int r_dtype, const void
     a.dy = (uint16_t*)dy;
     a.dr = dr;
     a.partial = (float*)ws;
+    a.stats = a.partial + (size_t)3 * blocks * K;
     if (M > 0 && launch_residual_norm_backward(a, (hipStream_t)stream) != hipSuccess)
         return QLL_ERR_HIP;
     const ColsumArgs c = {a.partial, blocks, (int)K, {dw_pre, dw_post, dgate}};

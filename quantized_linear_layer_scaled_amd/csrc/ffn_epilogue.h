@@ -85,17 +85,22 @@ __device__ __forceinline__ void with_act(int act, F&& f)
     }
 }
 
-// W consecutive bf16 values (W = 4 or 8, aligned to their size) <-> floats
+// Vectors of 32-bit words at any 2-byte address: rows of an odd number of
+// columns start anywhere, and the memory takes such accesses as they are.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+
+// W consecutive bf16 values (W = 4 or 8) <-> floats
 template <int W>
 __device__ __forceinline__ void load_bf16(const uint16_t* p, float* f)
 {
     static_assert(W == 4 || W == 8, "vector width");
     uint32_t w[W / 2];
     if constexpr (W == 8) {
-        const uint4 v = *(const uint4*)p;
+        const u32x4_any v = *(const u32x4_any*)p;
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else {
-        const uint2 v = *(const uint2*)p;
+        const u32x2_any v = *(const u32x2_any*)p;
         w[0] = v.x; w[1] = v.y;
     }
 #pragma unroll
@@ -107,26 +112,30 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float* f)
 // NT: a non-temporal store, for outputs that all compute units write at the
 // same time at the end of their tiles: plain ones wait, dirty, in L2 and slow
 // the next tile's first copies (forward products at M = 8192, N = 12288,
-// K = 4096: 1-7% less with NT).
+// K = 4096: 1-7% less with NT; 8-byte vectors and outputs that the next
+// product reads: 2-3% more).
 template <int W, bool NT = false>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float* f)
 {
     static_assert(W == 4 || W == 8, "vector width");
-    if constexpr (W == 8 && NT)
-        store16_stream(p, bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
-                       bf16x2_rne(f[6], f[7]));
-    else if constexpr (W == 8)
-        *(uint4*)p = make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
-                                bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7]));
-    else
-        *(uint2*)p = make_uint2(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]));
+    if constexpr (W == 8) {
+        const u32x4_any v = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
+                             bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, (u32x4_any*)p);
+        else
+            *(u32x4_any*)p = v;
+    } else {
+        *(u32x2_any*)p = u32x2_any{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])};
+    }
 }
 template <int W>
 __device__ __forceinline__ void store_f32(float* p, const float* f)
 {
+    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
     for (int i = 0; i < W; i += 4)
-        *(float4*)(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        *(f32x4_any*)(p + i) = f32x4_any{f[i], f[i + 1], f[i + 2], f[i + 3]};
 }
 
 // bf16_rne of one value, a NaN kept (bf16_rne is for finite values and
@@ -156,107 +165,107 @@ __device__ __forceinline__ void store_value(const FfnArgs& a, float v, int r, in
         ((uint16_t*)base)[i] = bf16_one(v);
 }
 
-// The same columns where rows are not whole vectors (C % W != 0): element by
-// element.  EPI_DZ, EPI_DGATED and EPI_PLAIN take whole vectors only.
+// What the columns of one vector share: their scales and biases, read once
+// (columns past the end stay 0).
+template <int W>
+struct ColumnVector {
+    float s0[W], s1[W], b[W];
+};
 template <int EPI, int W>
-__device__ __forceinline__ void ffn_store_ragged(const FfnArgs& a, const float* v, const float* u,
-                                                 int r, int c)
+__device__ __forceinline__ void load_columns(const FfnArgs& a, int c, ColumnVector<W>& v)
 {
-    if (r >= a.R)
-        return;
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_DZ) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int ci = c + i;
-        if (ci >= a.C)
-            continue;
-        if constexpr (EPI == EPI_PARTIAL) {
-            a.partial[((size_t)blockIdx.y * a.R + r) * a.C + ci] = v[i];
-        } else if constexpr (EPI == EPI_LINEAR) {
-            store_value(a, linear_value(a, v[i], r, ci), r, ci);
-        } else if constexpr (EPI == EPI_GATED) {
-            float g = v[i], up = u[i];
-            if (a.sq) {
-                g = g * a.sq[r] * a.sp[0][ci];
-                up = up * a.sq[r] * a.sp[1][ci];
+        for (int i = 0; i < W; ++i) {
+            v.s0[i] = v.s1[i] = v.b[i] = 0.0f;
+            if (c + i >= a.C)
+                continue;
+            if (EPI != EPI_DZ && a.sq) {
+                v.s0[i] = a.sp[0][c + i];
+                if (EPI == EPI_GATED)
+                    v.s1[i] = a.sp[1][c + i];
             }
-            with_act(a.act, [&](auto A) { g = act_value<decltype(A)::value>(g); });
-            store_value(a, g * up, r, ci);
+            if (EPI != EPI_GATED && a.bias)
+                v.b[i] = bf16_value(a.bias[c + i]);
         }
     }
 }
 
 // The W output columns c .. c + W - 1 of row r, whose fp32 sums are v (gated:
-// the gate's, u the up projection's); rows are whole vectors (C % W == 0), so
-// the vector is in range as a whole and aligned.  EPI_DZ adds its outputs to
-// cs.
+// the gate's, u the up projection's).  A vector that reaches past the last
+// column is stored element by element.  EPI_DZ adds its outputs to cs.
+// (EPI_DZ, EPI_DGATED and EPI_PLAIN have C % 8 == 0.)
 template <int EPI, int W, int ACT>
 __device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const float* u, int r,
-                                              int c, float* cs)
+                                              int c, const ColumnVector<W>& cv, float* cs)
 {
-    if (r >= a.R)
+    if (r >= a.R || c >= a.C)
         return;
-    if (c >= a.C)
-        return;
+    const bool whole = c + W <= a.C;
     if constexpr (EPI == EPI_PARTIAL) {
-        store_f32<W>(a.partial + ((size_t)blockIdx.y * a.R + r) * a.C + c, v);
+        float* o = a.partial + ((size_t)blockIdx.y * a.R + r) * a.C + c;
+        if (whole) {
+            store_f32<W>(o, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (c + i < a.C)
+                    o[i] = v[i];
+        }
     } else if constexpr (EPI == EPI_PLAIN) {
         uint16_t* base = (uint16_t*)(r < a.row_split ? a.out : a.out2);
         store_bf16<W>(base + (size_t)(r < a.row_split ? r : r - a.row_split) * a.ldo + c, v);
-    } else if constexpr (EPI == EPI_LINEAR) {
-        if (a.sq) {
-            const float s = a.sq[r];
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                v[i] = v[i] * s * a.sp[0][c + i];
-        }
-        if (a.bias) {
-            float b[W];
-            load_bf16<W>(a.bias + c, b);
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                v[i] += b[i];
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            v[i] = act_value<ACT>(v[i]);
-        if (a.res) {
-            float b[W];
-            load_bf16<W>(a.res + (size_t)r * a.C + c, b);
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                v[i] += b[i];
-        }
-        char* base = (char*)(r < a.row_split ? a.out : a.out2);
-        const size_t at = (size_t)(r < a.row_split ? r : r - a.row_split) * a.ldo + c;
-        if (a.out_fp32)
-            store_f32<W>((float*)base + at, v);
-        else
-            store_bf16<W, true>((uint16_t*)base + at, v);
-    } else if constexpr (EPI == EPI_GATED) {
-        float o[W];
+    } else if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
         const float s = a.sq ? a.sq[r] : 1.0f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float g = v[i], up = u[i];
-            if (a.sq) {
-                g = g * s * a.sp[0][c + i];
-                up = up * s * a.sp[1][c + i];
+            float z = v[i];
+            if (a.sq)
+                z = z * s * cv.s0[i];
+            if constexpr (EPI == EPI_LINEAR) {
+                v[i] = act_value<ACT>(a.bias ? z + cv.b[i] : z);
+            } else {
+                float up = u[i];
+                if (a.sq)
+                    up = up * s * cv.s1[i];
+                v[i] = act_value<ACT>(z) * up;
             }
-            o[i] = act_value<ACT>(g) * up;
         }
-        if (a.out_fp32)
-            store_f32<W>((float*)a.out + (size_t)r * a.ldo + c, o);
-        else
-            store_bf16<W, true>((uint16_t*)a.out + (size_t)r * a.ldo + c, o);
+        if (EPI == EPI_LINEAR && a.res) {
+            const uint16_t* from = a.res + (size_t)r * a.C + c;
+            if (whole) {
+                float b[W];
+                load_bf16<W>(from, b);
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    v[i] += b[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    if (c + i < a.C)
+                        v[i] += bf16_value(from[i]);
+            }
+        }
+        char* base = (char*)(r < a.row_split ? a.out : a.out2);
+        const size_t at = (size_t)(r < a.row_split ? r : r - a.row_split) * a.ldo + c;
+        if (whole) {
+            if (a.out_fp32)
+                store_f32<W>((float*)base + at, v);
+            else
+                store_bf16<W, true>((uint16_t*)base + at, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (c + i < a.C)
+                    store_value(a, v[i], r, c + i);
+        }
     } else if constexpr (EPI == EPI_DZ) {
-        float b[W], d[W];
+        float d[W];
         load_bf16<W>(a.dy + (size_t)r * a.C + c, d);
-        if (a.bias)
-            load_bf16<W>(a.bias + c, b);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float f, sl;
-            act_slope<ACT>(a.bias ? v[i] + b[i] : v[i], f, sl);
+            act_slope<ACT>(a.bias ? v[i] + cv.b[i] : v[i], f, sl);
             d[i] *= sl;
             cs[i] += d[i];
         }

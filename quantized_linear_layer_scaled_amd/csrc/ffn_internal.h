@@ -106,14 +106,16 @@ struct NormArgs {
     uint16_t* dy;           // bf16 [M][K] (null without y)
     void* dr;               // [M][K], type of r
     float* partial;         // [3][blocks][K]: dw_pre, dw_post, dgate sums
+    float* stats;           // [M][4]: 1 / rms(y), 1 / rms(h), mean term (long rows)
     float alpha, beta, eps;
     int M, K;
     int r_fp32, quant;
 };
 constexpr int kNormMaxK = 32768;
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
-// Workgroups of the backward kernel = rows of each partial sum.
+// Rows of each partial sum, and floats of statistics, of the backward pass.
 int norm_backward_blocks(int64_t M, int64_t K);
+int64_t norm_backward_stats(int64_t M, int64_t K);
 hipError_t launch_residual_norm_backward(const NormArgs& a, hipStream_t stream);
 
 }  // namespace qll

@@ -5,31 +5,45 @@
 
 namespace qll {
 
-// 0: 256x256 over 8 waves, 1: 128x128 over 4, 2: 64x64 over 4.
-constexpr int kFfnTile[3] = {256, 128, 64};
-constexpr int kFfnWaveRows[3] = {2, 2, 2};  // waves along the output's rows
+// Rows and columns of the tiles, and waves along the rows.
+struct FfnTile {
+    int rows, cols, wave_rows;
+};
+constexpr FfnTile kFfnTiles[] = {{256, 256, 2}, {128, 128, 2}, {128, 128, 4}, {64, 64, 2}};
+constexpr int kFfnSmallest = 3;
 
-int ffn_tile_pick(int64_t R, int64_t C, int epi);
+inline int64_t ffn_tiles(int tile, int64_t R, int64_t C, int epi)
+{
+    const bool dual = epi == EPI_GATED || epi == EPI_DGATED;
+    const int64_t TR = kFfnTiles[tile].rows, TC = kFfnTiles[tile].cols / (dual ? 2 : 1);
+    return ((R + TR - 1) / TR) * ((C + TC - 1) / TC);
+}
 
 template <bool FP8, int LAY, int EPI>
 hipError_t ffn_launch_tile(int tile, const FfnArgs& a, hipStream_t stream)
 {
-    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
-    const int B = kFfnTile[tile];
-    const int64_t tiles = (int64_t)((a.R + B - 1) / B) * ((a.C + (DUAL ? B / 2 : B) - 1) / (DUAL ? B / 2 : B));
-    const dim3 grid((unsigned)tiles, (unsigned)a.splits);
+    const int64_t tiles = ffn_tiles(tile, a.R, a.C, EPI);
     if constexpr (EPI != EPI_PARTIAL) {  // (only the smallest tile splits K)
-        if (tile == 0) {
+        switch (tile) {
+        case 0:
             // one workgroup per CU
             ffn_alt_kernel<FP8, LAY, EPI>
                 <<<(unsigned)(tiles < 256 ? tiles : 256), 512, 0, stream>>>(a);
             return hipGetLastError();
+        case 1:
+            // two workgroups per CU
+            ffn_ring_kernel<FP8, LAY, EPI, 128, 128, 2, 2, 2>
+                <<<(unsigned)tiles, 256, 0, stream>>>(a);
+            return hipGetLastError();
+        case 2:
+            // one workgroup per CU, three stages of copies in flight
+            ffn_ring_kernel<FP8, LAY, EPI, 128, 128, 2, 4, 4>
+                <<<(unsigned)tiles, 512, 0, stream>>>(a);
+            return hipGetLastError();
         }
     }
-    if (tile == 1)
-        ffn_ring_kernel<FP8, LAY, EPI, 128, 128, 2, 2, 2><<<grid, 256, 0, stream>>>(a);
-    else
-        ffn_ring_kernel<FP8, LAY, EPI, 64, 64, 2, 2, 4><<<grid, 256, 0, stream>>>(a);
+    ffn_ring_kernel<FP8, LAY, EPI, 64, 64, 2, 2, 4>
+        <<<dim3((unsigned)tiles, (unsigned)a.splits), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

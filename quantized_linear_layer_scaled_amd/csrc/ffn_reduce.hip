@@ -24,8 +24,10 @@ __global__ __launch_bounds__(256) void ffn_reduce_kernel(FfnArgs a)
             v[2] += p.z;
             v[3] += p.w;
         }
+        ColumnVector<4> cv;
+        load_columns<EPI_LINEAR, 4>(a, c, cv);
         with_act(a.act, [&](auto A) {
-            ffn_store_act<EPI_LINEAR, 4, decltype(A)::value>(a, v, nullptr, r, c, nullptr);
+            ffn_store_act<EPI_LINEAR, 4, decltype(A)::value>(a, v, nullptr, r, c, cv, nullptr);
         });
     } else {
         float v = 0.0f;

@@ -11,33 +11,37 @@ hipError_t ffn_launch_nt_grad(int, int, const FfnArgs&, hipStream_t);
 hipError_t ffn_launch_nn(int, int, const FfnArgs&, hipStream_t);
 hipError_t ffn_launch_tn(int, int, const FfnArgs&, hipStream_t);
 
-// The largest tile that still gives every compute unit one.
+// Measured per call (us): the 256x256 tile against the 128x128 ones, gated FP8
+// M = 1024, N = 6144, K = 2048 (192 tiles of the 256 CUs): 28 / 36; FP8
+// M = 2048, N = 4096, K = 12288 (128 tiles): 121 / 97.  128x128 over 4 waves,
+// two workgroups per CU, against 8 waves and a deeper ring: bf16 M = 1024,
+// N = K = 4096 (256 tiles) 55.7 / 46.8; gated bf16 M = 300, N = 6144, K = 2048
+// (288 tiles) 30.2 / 48.5.  128x128 against 64x64: M = 512, N = 4096, K = 2048
+// (128 tiles) 26.1 / 23.3.
 int ffn_tile_pick(int64_t R, int64_t C, int epi)
 {
-    const bool dual = epi == EPI_GATED || epi == EPI_DGATED;
-    for (int t = 0; t < 2; ++t) {
-        const int64_t B = kFfnTile[t], TC = dual ? B / 2 : B;
-        if (((R + B - 1) / B) * ((C + TC - 1) / TC) >= 256)
-            return t;
-    }
-    return 2;
+    if (ffn_tiles(0, R, C, epi) >= 176)
+        return 0;
+    const int64_t n = ffn_tiles(1, R, C, epi);
+    return n > 256 ? 1 : (n >= 192 ? 2 : kFfnSmallest);
 }
 
 int ffn_dz_strips(int64_t R, int64_t C)
 {
-    const int t = ffn_tile_pick(R, C, EPI_DZ);
-    return (int)((R + kFfnTile[t] - 1) / kFfnTile[t]) * kFfnWaveRows[t];
+    const FfnTile& t = kFfnTiles[ffn_tile_pick(R, C, EPI_DZ)];
+    return (int)((R + t.rows - 1) / t.rows) * t.wave_rows;
 }
 
+// Split-K: about three workgroups per CU, of at least 16 stages each (input
+// gradient M = 512, N = 6144, K = 2048: 43 us unsplit, 36 with two pieces, 37
+// with four; M = 256, N = 2048, K = 6144: 44, 28, 23).
 int ffn_splits(int64_t R, int64_t C, int64_t stages)
 {
-    const int t = ffn_tile_pick(R, C, EPI_LINEAR);
-    const int64_t B = kFfnTile[t];
-    const int64_t tiles = ((R + B - 1) / B) * ((C + B - 1) / B);
-    if (t != 2 || tiles >= 256 || stages < 16)
+    const int64_t tiles = ffn_tiles(kFfnSmallest, R, C, EPI_LINEAR);
+    if (tiles == 0 || ffn_tile_pick(R, C, EPI_LINEAR) != kFfnSmallest)
         return 1;
-    int64_t s = 512 / tiles;
-    s = s < stages / 8 ? s : stages / 8;
+    const int64_t by_tiles = 768 / tiles;
+    const int64_t s = by_tiles < stages / 16 ? by_tiles : stages / 16;
     return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
 }
 

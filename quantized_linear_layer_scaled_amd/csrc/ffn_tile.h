@@ -191,24 +191,16 @@ __device__ __forceinline__ void ffn_finish(const FfnArgs& a, v4f (&acc)[2][SP::N
             }
         }
     };
-    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_PARTIAL) {
-        if (a.C % W != 0) {
-            columns([&](int h, int jv, int c) __attribute__((always_inline)) {
-                rows(h, jv, [&](float* v, float* u, int r) __attribute__((always_inline)) {
-                    ffn_store_ragged<EPI, W>(a, v, u, r, c);
-                });
-            });
-            return;
-        }
-    }
     auto run = [&](auto A) __attribute__((always_inline)) {
         columns([&](int h, int jv, int c) __attribute__((always_inline)) {
             float cs[W];
 #pragma unroll
             for (int e = 0; e < W; ++e)
                 cs[e] = 0.0f;
+            ColumnVector<W> cv;
+            load_columns<EPI, W>(a, c, cv);
             rows(h, jv, [&](float* v, float* u, int r) __attribute__((always_inline)) {
-                ffn_store_act<EPI, W, decltype(A)::value>(a, v, u, r, c, cs);
+                ffn_store_act<EPI, W, decltype(A)::value>(a, v, u, r, c, cv, cs);
             });
             if constexpr (EPI == EPI_DZ) {
                 // the wave's column sums over its rows (16 lanes share a

@@ -49,18 +49,34 @@ __device__ __forceinline__ float row_reduce(float v, float* red)
     return v;
 }
 
+// Eight values of the stream as they lie in memory, and as floats.
 template <bool F32>
-__device__ __forceinline__ void load_stream(const void* p, size_t at, float* f)
-{
-    if constexpr (F32) {
-        const float4 x = *(const float4*)((const float*)p + at);
-        const float4 y = *(const float4*)((const float*)p + at + 4);
-        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-    } else {
-        load_bf16<8>((const uint16_t*)p + at, f);
+struct StreamRun {
+    uint4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int p = 0; p < (F32 ? 2 : 1); ++p)
+            w[p] = make_uint4(0, 0, 0, 0);
     }
-}
+    __device__ __forceinline__ void load(const void* base, size_t at)
+    {
+#pragma unroll
+        for (int p = 0; p < (F32 ? 2 : 1); ++p)
+            w[p] = *(const uint4*)((const char*)base + (F32 ? (at + 4 * p) * 4 : at * 2));
+    }
+    __device__ __forceinline__ void widen(float* f) const
+    {
+        if constexpr (F32) {
+            const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = __uint_as_float(v[e]);
+        } else {
+            unpack8(w[0], f);
+        }
+    }
+};
 
 template <bool F32>
 __device__ __forceinline__ void store_stream(void* p, size_t at, const float* f)
@@ -71,6 +87,36 @@ __device__ __forceinline__ void store_stream(void* p, size_t at, const float* f)
         store_bf16<8>((uint16_t*)p + at, f);
 }
 
+// A thread's runs of the three channel vectors (missing ones read as 1), kept
+// in registers over the rows where there is one run per thread, else read
+// again for each row.
+template <int T, int CH>
+struct Vectors {
+    static constexpr bool KEEP = CH == 1;
+    const NormArgs& a;
+    int t;
+    uint4 kept[3];
+    __device__ __forceinline__ Vectors(const NormArgs& args, int tid) : a(args), t(tid)
+    {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int v = 0; v < 3; ++v)
+                kept[v] = fetch(v, 0);
+        }
+    }
+    __device__ __forceinline__ uint4 fetch(int v, int j) const
+    {
+        const uint16_t* p = v == 0 ? a.w_post : (v == 1 ? a.gate : a.w_pre);
+        const int c = (t + j * T) * 8;
+        return p && c < a.K ? *(const uint4*)(p + c)
+                            : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    }
+    __device__ __forceinline__ void get(int v, int j, float* f) const
+    {
+        unpack8(KEEP ? kept[v] : fetch(v, j), f);
+    }
+};
+
 __device__ __forceinline__ float inv_rms(float sum, int K, float eps)
 {
     return 1.0f / sqrtf(sum / (float)K + eps);
@@ -78,243 +124,267 @@ __device__ __forceinline__ float inv_rms(float sum, int K, float eps)
 
 }  // namespace
 
-// T threads per row, CH runs of 8 columns per thread; rows of up to 64
-// threads share a workgroup of 256.
+// One row at a time per workgroup of T threads, CH runs of 8 columns per
+// thread, rows blockIdx.x, + gridDim.x, ...  The next row's words are loaded
+// before this row's sums are formed (one run per thread; longer rows have no
+// registers for it).
 template <int T, int CH, bool HAS_Y, bool F32, bool QUANT>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void residual_norm_kernel(NormArgs a)
+__global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a)
 {
-    constexpr int TB = T < 256 ? 256 : T;
-    static_assert(T == 64 || T >= 256, "threads of a row");
-    __shared__ float red[3][TB / 64];
-    const int t = threadIdx.x % T;
-    const int m = blockIdx.x * (TB / T) + threadIdx.x / T;
-    if (T < 256 && m >= a.M)
-        return;  // (whole waves; rows of 64 threads meet no barrier)
-    const int K = a.K;
-    const size_t row = (size_t)m * K;
-
-    float h[CH][8];
-    float y[HAS_Y ? CH : 1][8];
-    float sy = 0.0f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int c = (t + j * T) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            h[j][e] = 0.0f;
-        if (c < K)
-            load_stream<F32>(a.r, row + c, h[j]);
-        if constexpr (HAS_Y) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                y[j][e] = 0.0f;
-            if (c < K)
-                load_bf16<8>(a.y + row + c, y[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sy += y[j][e] * y[j][e];
-        }
-    }
-    float sh = 0.0f;
-    if constexpr (HAS_Y) {
-        float iy = 1.0f;
-        if (a.w_post)
-            iy = inv_rms(row_reduce<T, false>(sy, red[0]), K, a.eps);
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = (t + j * T) * 8;
-            if (c < K) {
-                float w[8];
-                if (a.w_post) {
-                    load_bf16<8>(a.w_post + c, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[j][e] = y[j][e] * iy * w[e];
-                }
-                if (a.gate) {
-                    load_bf16<8>(a.gate + c, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[j][e] *= w[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    h[j][e] = a.alpha * h[j][e] + a.beta * y[j][e];
-                store_stream<F32>(a.r_out, row + c, h[j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sh += h[j][e] * h[j][e];
-    const float ih = inv_rms(row_reduce<T, false>(sh, red[1]), K, a.eps);
-    float amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int c = (t + j * T) * 8;
-        if (c < K) {
-            float w[8];
-            load_bf16<8>(a.w_pre + c, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[j][e] = h[j][e] * ih * w[e];
-                amax = fmaxf(amax, fabsf(h[j][e]));
-            }
-            if constexpr (!QUANT)
-                store_bf16<8>((uint16_t*)a.n_out + row + c, h[j]);
-        }
-    }
-    if constexpr (QUANT) {
-        // the rule of quantize_per_token_fp8, on the fp32 values
-        amax = row_reduce<T, true>(amax, red[2]);
-        const Quot q(amax / 448.0f);
-        if (t == 0)
-            a.n_scales[m] = q.s;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = (t + j * T) * 8;
-            if (c < K) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] = q.s == 0.0f ? 0.0f
-                                       : clamp448(q.fast ? q.by_reciprocal(h[j][e]) : h[j][e] / q.s);
-                int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-                w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w0, true);
-                int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
-                w1 = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], w1, true);
-                *(uint2*)((uint8_t*)a.n_out + row + c) = make_uint2((uint32_t)w0, (uint32_t)w1);
-            }
-        }
-    }
-}
-
-// One row at a time per workgroup of T threads, rows blockIdx.x, + gridDim.x,
-// ...; the vector gradients' sums stay in registers.
-template <int T, int CH, bool HAS_Y, bool F32>
-__global__ __launch_bounds__(T) void residual_norm_backward_kernel(NormArgs a)
-{
-    __shared__ float red[2][4][T / 64];
+    __shared__ float red[2][3][T / 64];
+    constexpr bool AHEAD = CH == 1;
     const int t = threadIdx.x;
     const int K = a.K;
-    const float invk = 1.0f / (float)K;
-    float s_pre[CH][8], s_post[HAS_Y ? CH : 1][8], s_gate[HAS_Y ? CH : 1][8];
+    const Vectors<T, CH> vec(a, t);
+    struct Row {
+        uint4 y[CH];
+        StreamRun<F32> r[CH];
+    } next;
+    auto fetch = [&](int m) __attribute__((always_inline)) {
+        const size_t row = (size_t)m * K;
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s_pre[j][e] = 0.0f;
-            if constexpr (HAS_Y)
-                s_post[j][e] = s_gate[j][e] = 0.0f;
+        for (int j = 0; j < CH; ++j) {
+            const int c = (t + j * T) * 8;
+            next.y[j] = make_uint4(0, 0, 0, 0);
+            next.r[j].clear();
+            if (m < a.M && c < K) {
+                next.r[j].load(a.r, row + c);
+                if constexpr (HAS_Y)
+                    next.y[j] = *(const uint4*)(a.y + row + c);
+            }
         }
+    };
+    if constexpr (AHEAD)
+        fetch(blockIdx.x);
     int par = 0;
     for (int m = blockIdx.x; m < a.M; m += gridDim.x, par ^= 1) {
         const size_t row = (size_t)m * K;
-        float h[CH][8], u[CH][8], d[CH][8], y[HAS_Y ? CH : 1][8];
-        float sy = 0.0f;
+        if constexpr (!AHEAD)
+            fetch(m);
+        float h[CH][8], y[HAS_Y ? CH : 1][8];
+        float sy = 0.0f, sh = 0.0f;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = (t + j * T) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[j][e] = u[j][e] = d[j][e] = 0.0f;
-                if constexpr (HAS_Y)
-                    y[j][e] = 0.0f;
-            }
-            if (c < K) {
-                load_stream<F32>(a.r, row + c, h[j]);
-                load_bf16<8>(a.dn + row + c, u[j]);
-                if (a.dr_out)
-                    load_stream<F32>(a.dr_out, row + c, d[j]);
-                if constexpr (HAS_Y)
-                    load_bf16<8>(a.y + row + c, y[j]);
-            }
+            next.r[j].widen(h[j]);
             if constexpr (HAS_Y) {
+                unpack8(next.y[j], y[j]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     sy += y[j][e] * y[j][e];
             }
         }
-        float iy = 1.0f;
+        if constexpr (AHEAD)
+            fetch(m + gridDim.x);
         if constexpr (HAS_Y) {
+            float iy = 1.0f;
             if (a.w_post)
                 iy = inv_rms(row_reduce<T, false>(sy, red[par][0]), K, a.eps);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = (t + j * T) * 8;
+                float w1[8], g[8];
+                vec.get(0, j, w1);
+                vec.get(1, j, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[j][e] = a.alpha * h[j][e] + a.beta * (y[j][e] * iy * w1[e] * g[e]);
+                if (c < K)
+                    store_stream<F32>(a.r_out, row + c, h[j]);
+            }
         }
-        float sh = 0.0f, suh = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sh += h[j][e] * h[j][e];
+        const float ih = inv_rms(row_reduce<T, false>(sh, red[par][1]), K, a.eps);
+        float amax = 0.0f;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = (t + j * T) * 8;
-            if (c < K) {
-                float w[8];
-                if constexpr (HAS_Y) {
-                    float p[8];
+            float w2[8];
+            vec.get(2, j, w2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[j][e] = h[j][e] * ih * w2[e];
+                amax = fmaxf(amax, fabsf(h[j][e]));
+            }
+            if constexpr (!QUANT) {
+                if (c < K)
+                    store_bf16<8>((uint16_t*)a.n_out + row + c, h[j]);
+            }
+        }
+        if constexpr (QUANT) {
+            // the rule of quantize_per_token_fp8, on the fp32 values
+            amax = row_reduce<T, true>(amax, red[par][2]);
+            const Quot q(amax / 448.0f);
+            if (t == 0)
+                a.n_scales[m] = q.s;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = (t + j * T) * 8;
+                float f[8];
+                if (q.fast) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        p[e] = y[j][e];
-                    if (a.w_post) {
-                        load_bf16<8>(a.w_post + c, w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            p[e] = y[j][e] * iy * w[e];
-                    }
-                    if (a.gate) {
-                        load_bf16<8>(a.gate + c, w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            p[e] *= w[e];
-                    }
+                        f[e] = clamp448(q.by_reciprocal(h[j][e]));
+                } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        h[j][e] = a.alpha * h[j][e] + a.beta * p[e];
+                        f[e] = q.s == 0.0f ? 0.0f : clamp448(h[j][e] / q.s);
                 }
-                load_bf16<8>(a.w_pre + c, w);
+                int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+                w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w0, true);
+                int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
+                w1 = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], w1, true);
+                if (c < K)
+                    *(uint2*)((uint8_t*)a.n_out + row + c) = make_uint2((uint32_t)w0, (uint32_t)w1);
+            }
+        }
+    }
+}
+
+// Rows as above; the vector gradients' sums stay in registers.  The rows are
+// kept as they lie in memory and widened in each of the three passes over
+// them, which leaves the registers for the sums.
+//
+// SUMS false (rows of more than 8192 columns, whose sums do not fit in the
+// registers: with them K = 16384, M = 4096 spills and takes 415 us and more,
+// against 156 us of memory traffic): the rows' statistics go to a.stats, and
+// residual_norm_vectors_kernel forms the vector gradients from them.
+template <int T, int CH, bool HAS_Y, bool F32, bool SUMS>
+__global__ __launch_bounds__(T) void residual_norm_backward_kernel(NormArgs a)
+{
+    __shared__ float red[2][4][T / 64];
+    constexpr bool AHEAD = SUMS && CH <= 2;
+    const int t = threadIdx.x;
+    const int K = a.K;
+    const float invk = 1.0f / (float)K;
+    const Vectors<T, CH> vec(a, t);
+    constexpr int SCH = SUMS ? CH : 1;
+    float s_pre[SCH][8], s_post[SCH][8], s_gate[SCH][8];
+#pragma unroll
+    for (int j = 0; j < SCH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s_pre[j][e] = s_post[j][e] = s_gate[j][e] = 0.0f;
+    struct Row {
+        uint4 y[HAS_Y ? CH : 1], u[CH];
+        StreamRun<F32> r[CH], d[CH];
+    } next;
+    auto fetch = [&](int m) __attribute__((always_inline)) {
+        const size_t row = (size_t)m * K;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = (t + j * T) * 8;
+            next.u[j] = make_uint4(0, 0, 0, 0);
+            if constexpr (HAS_Y)
+                next.y[j] = make_uint4(0, 0, 0, 0);
+            next.r[j].clear();
+            next.d[j].clear();
+            if (m < a.M && c < K) {
+                next.u[j] = *(const uint4*)(a.dn + row + c);
+                if constexpr (HAS_Y)
+                    next.y[j] = *(const uint4*)(a.y + row + c);
+                next.r[j].load(a.r, row + c);
+                if (a.dr_out)
+                    next.d[j].load(a.dr_out, row + c);
+            }
+        }
+    };
+    if constexpr (AHEAD)
+        fetch(blockIdx.x);
+    int par = 0;
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x, par ^= 1) {
+        const size_t row = (size_t)m * K;
+        if constexpr (!AHEAD)
+            fetch(m);
+        const Row now = next;
+        if constexpr (AHEAD)
+            fetch(m + gridDim.x);
+        float iy = 1.0f;
+        if constexpr (HAS_Y) {
+            if (a.w_post) {
+                float sy = 0.0f;
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    float y[8];
+                    unpack8(now.y[j], y);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sy += y[e] * y[e];
+                }
+                iy = inv_rms(row_reduce<T, false>(sy, red[par][0]), K, a.eps);
+            }
+        }
+        // h of run j, and the normed y times w_post (p) where there is a y
+        auto stream = [&](int j, float* h, float* p) __attribute__((always_inline)) {
+            now.r[j].widen(h);
+            if constexpr (HAS_Y) {
+                float w1[8], g[8];
+                unpack8(now.y[j], p);
+                vec.get(0, j, w1);
+                vec.get(1, j, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    sh += h[j][e] * h[j][e];
-                    suh += u[j][e] * w[e] * h[j][e];
+                    p[e] = p[e] * iy * w1[e];
+                    h[e] = a.alpha * h[e] + a.beta * (p[e] * g[e]);
                 }
+            }
+        };
+        float sh = 0.0f, suh = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float h[8], p[8], u[8], w2[8];
+            stream(j, h, p);
+            unpack8(now.u[j], u);
+            vec.get(2, j, w2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sh += h[e] * h[e];
+                suh += u[e] * w2[e] * h[e];
             }
         }
         sh = row_reduce<T, false>(sh, red[par][1]);
         suh = row_reduce<T, false>(suh, red[par][2]);
         const float ih = inv_rms(sh, K, a.eps);
         const float mh = suh * invk * ih * ih;
+        if (!SUMS && t == 0)
+            *(float4*)(a.stats + 4 * (size_t)m) = make_float4(iy, ih, mh, 0.0f);
         float svy = 0.0f;
+        float v[HAS_Y ? CH : 1][8];  // dy before the post-norm's own term
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int c = (t + j * T) * 8;
-            if (c < K) {
-                float w[8], o[8];
-                load_bf16<8>(a.w_pre + c, w);
+            float h[8], p[8], u[8], w2[8], d[8], o[8];
+            stream(j, h, p);
+            unpack8(now.u[j], u);
+            vec.get(2, j, w2);
+            now.d[j].widen(d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (SUMS)
+                    s_pre[j][e] += u[e] * h[e] * ih;
+                d[e] += ih * (u[e] * w2[e] - h[e] * mh);
+                o[e] = a.alpha * d[e];
+            }
+            if (c < K)
+                store_stream<F32>(a.dr, row + c, o);
+            if constexpr (HAS_Y) {
+                float w1[8], g[8], y[8];
+                vec.get(0, j, w1);
+                vec.get(1, j, g);
+                unpack8(now.y[j], y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    s_pre[j][e] += u[j][e] * h[j][e] * ih;
-                    d[j][e] += ih * (u[j][e] * w[e] - h[j][e] * mh);
-                    o[e] = a.alpha * d[j][e];
-                }
-                store_stream<F32>(a.dr, row + c, o);
-                if constexpr (HAS_Y) {
-                    float w1[8], g[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        w1[e] = g[e] = 1.0f;
-                        d[j][e] *= a.beta;
+                    const float dt = a.beta * d[e];
+                    const float dp = dt * g[e];
+                    if constexpr (SUMS) {
+                        s_gate[j][e] += dt * p[e];
+                        s_post[j][e] += dp * (y[e] * iy);
                     }
-                    if (a.w_post)
-                        load_bf16<8>(a.w_post + c, w1);
-                    if (a.gate)
-                        load_bf16<8>(a.gate + c, g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float yn = y[j][e] * iy;
-                        s_gate[j][e] += d[j][e] * yn * w1[e];
-                        d[j][e] *= g[e];
-                        s_post[j][e] += d[j][e] * yn;
-                        d[j][e] *= w1[e];
-                        svy += d[j][e] * y[j][e];
-                    }
+                    v[j][e] = dp * w1[e];
+                    svy += v[j][e] * y[e];
                 }
             }
         }
@@ -325,30 +395,92 @@ __global__ __launch_bounds__(T) void residual_norm_backward_kernel(NormArgs a)
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const int c = (t + j * T) * 8;
-                if (c < K) {
-                    float o[8];
+                float y[8], o[8];
+                unpack8(now.y[j], y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[e] = iy * (d[j][e] - y[j][e] * my);
+                for (int e = 0; e < 8; ++e)
+                    o[e] = iy * (v[j][e] - y[e] * my);
+                if (c < K)
                     store_bf16<8>(a.dy + row + c, o);
+            }
+        }
+    }
+    if constexpr (SUMS) {
+        const size_t plane = (size_t)gridDim.x * K;
+        float* part = a.partial + (size_t)blockIdx.x * K;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = (t + j * T) * 8;
+            if (c < K) {
+                store_f32<8>(part + c, s_pre[j]);
+                if constexpr (HAS_Y) {
+                    if (a.w_post)
+                        store_f32<8>(part + plane + c, s_post[j]);
+                    if (a.gate)
+                        store_f32<8>(part + 2 * plane + c, s_gate[j]);
                 }
             }
         }
     }
-    const size_t plane = (size_t)gridDim.x * K;
-    float* part = a.partial + (size_t)blockIdx.x * K;
+}
+
+// The vector gradients' partial sums over rows blockIdx.x, + gridDim.x, ...
+// for 8 columns per thread, from the rows' statistics.
+template <bool HAS_Y, bool F32>
+__global__ __launch_bounds__(256) void residual_norm_vectors_kernel(NormArgs a)
+{
+    const int K = a.K;
+    const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
+    if (c >= K)
+        return;
+    const Vectors<256, 1> vec(a, c / 8);
+    float w1[8], g[8], w2[8];
+    vec.get(0, 0, w1);
+    vec.get(1, 0, g);
+    vec.get(2, 0, w2);
+    float s_pre[8], s_post[8], s_gate[8];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int c = (t + j * T) * 8;
-        if (c < K) {
-            store_f32<8>(part + c, s_pre[j]);
+    for (int e = 0; e < 8; ++e)
+        s_pre[e] = s_post[e] = s_gate[e] = 0.0f;
+#pragma unroll 2
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const size_t at = (size_t)m * K + c;
+        const float4 st = *(const float4*)(a.stats + 4 * (size_t)m);
+        const float iy = st.x, ih = st.y, mh = st.z;
+        StreamRun<F32> r, dr;
+        r.load(a.r, at);
+        dr.clear();
+        if (a.dr_out)
+            dr.load(a.dr_out, at);
+        float h[8], u[8], d[8], y[8];
+        r.widen(h);
+        dr.widen(d);
+        unpack8(*(const uint4*)(a.dn + at), u);
+        if constexpr (HAS_Y)
+            unpack8(*(const uint4*)(a.y + at), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float p = 0.0f;
             if constexpr (HAS_Y) {
-                if (a.w_post)
-                    store_f32<8>(part + plane + c, s_post[j]);
-                if (a.gate)
-                    store_f32<8>(part + 2 * plane + c, s_gate[j]);
+                p = y[e] * iy * w1[e];
+                h[e] = a.alpha * h[e] + a.beta * (p * g[e]);
+            }
+            s_pre[e] += u[e] * h[e] * ih;
+            if constexpr (HAS_Y) {
+                const float dt = a.beta * (d[e] + ih * (u[e] * w2[e] - h[e] * mh));
+                s_gate[e] += dt * p;
+                s_post[e] += dt * g[e] * (y[e] * iy);
             }
         }
+    }
+    const size_t plane = (size_t)gridDim.x * K;
+    float* part = a.partial + (size_t)blockIdx.x * K + c;
+    store_f32<8>(part, s_pre);
+    if constexpr (HAS_Y) {
+        if (a.w_post)
+            store_f32<8>(part + plane, s_post);
+        if (a.gate)
+            store_f32<8>(part + 2 * plane, s_gate);
     }
 }
 
@@ -357,11 +489,13 @@ namespace {
 template <int T, int CH>
 hipError_t forward(const NormArgs& a, hipStream_t s)
 {
-    constexpr int TB = T < 256 ? 256 : T;
-    const unsigned grid = (unsigned)((a.M + TB / T - 1) / (TB / T));
+    // as many workgroups as the compute units hold threads for; rows of
+    // several runs per thread gain nothing from a loop
+    constexpr int most = 256 * (2048 / T);
+    const unsigned grid = (unsigned)(a.M < most || CH > 1 ? a.M : most);
     auto go = [&](auto HY, auto F, auto Q) {
         residual_norm_kernel<T, CH, decltype(HY)::value, decltype(F)::value, decltype(Q)::value>
-            <<<grid, TB, 0, s>>>(a);
+            <<<grid, T, 0, s>>>(a);
     };
     using Y = std::true_type;
     using N = std::false_type;
@@ -378,20 +512,26 @@ hipError_t forward(const NormArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int T, int CH>
+template <int T, int CH, bool SUMS>
 hipError_t backward(const NormArgs& a, hipStream_t s)
 {
-    const unsigned grid = (unsigned)norm_backward_blocks(a.M, a.K);
-    if (a.y) {
-        if (a.r_fp32)
-            residual_norm_backward_kernel<T, CH, true, true><<<grid, T, 0, s>>>(a);
-        else
-            residual_norm_backward_kernel<T, CH, true, false><<<grid, T, 0, s>>>(a);
-    } else {
-        if (a.r_fp32)
-            residual_norm_backward_kernel<T, CH, false, true><<<grid, T, 0, s>>>(a);
-        else
-            residual_norm_backward_kernel<T, CH, false, false><<<grid, T, 0, s>>>(a);
+    const unsigned blocks = (unsigned)norm_backward_blocks(a.M, a.K);
+    const unsigned grid = SUMS ? blocks : (unsigned)a.M;
+    const dim3 strips(blocks, (unsigned)((a.K / 8 + 255) / 256));
+    auto go = [&](auto HY, auto F) {
+        residual_norm_backward_kernel<T, CH, decltype(HY)::value, decltype(F)::value, SUMS>
+            <<<grid, T, 0, s>>>(a);
+        if constexpr (!SUMS)
+            residual_norm_vectors_kernel<decltype(HY)::value, decltype(F)::value>
+                <<<strips, 256, 0, s>>>(a);
+    };
+    using Y = std::true_type;
+    using N = std::false_type;
+    switch ((a.y ? 2 : 0) + (a.r_fp32 ? 1 : 0)) {
+    case 0: go(N{}, N{}); break;
+    case 1: go(N{}, Y{}); break;
+    case 2: go(Y{}, N{}); break;
+    default: go(Y{}, Y{}); break;
     }
     return hipGetLastError();
 }
@@ -403,42 +543,49 @@ hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s)
     const int runs = a.K / 8;
     if (runs <= 64)
         return forward<64, 1>(a, s);
+    if (runs <= 128)
+        return forward<128, 1>(a, s);
     if (runs <= 256)
-        return a.M >= 1024 ? forward<64, 4>(a, s) : forward<256, 1>(a, s);
+        return forward<256, 1>(a, s);
     if (runs <= 512)
-        return a.M >= 1024 ? forward<256, 2>(a, s) : forward<512, 1>(a, s);
+        return forward<512, 1>(a, s);
     if (runs <= 1024)
-        return a.M >= 1024 ? forward<256, 4>(a, s) : forward<1024, 1>(a, s);
+        return forward<512, 2>(a, s);
     if (runs <= 2048)
         return forward<1024, 2>(a, s);
     return forward<1024, 4>(a, s);
 }
 
+// Rows of partial sums: workgroups of the backward kernel, what one wave of
+// workgroups with 200-odd registers fills.  More of them cost more partial
+// sums than they hide (M = 1024, K = 4096: 256 workgroups 21.8 us, 512 27.5,
+// 1024 35.8; M = 8192, K = 2048: 512 48.9, 1024 57.3).  Past 8192 columns,
+// strips of the vectors' kernel.
 int norm_backward_blocks(int64_t M, int64_t K)
 {
     const int64_t runs = K / 8;
-    const int64_t most = runs <= 256 ? 1024 : 512;
-    if (M <= most)
-        return (int)M;
-    return (int)most;
+    const int64_t most = runs <= 128 ? 1024 : (runs <= 256 ? 512 : (runs <= 1024 ? 256 : 128));
+    return (int)(M < most ? M : most);
 }
+
+int64_t norm_backward_stats(int64_t M, int64_t K) { return K > 8192 ? 4 * M : 0; }
 
 hipError_t launch_residual_norm_backward(const NormArgs& a, hipStream_t s)
 {
     const int runs = a.K / 8;
     if (runs <= 64)
-        return backward<64, 1>(a, s);
+        return backward<64, 1, true>(a, s);
     if (runs <= 128)
-        return backward<128, 1>(a, s);
+        return backward<128, 1, true>(a, s);
     if (runs <= 256)
-        return backward<256, 1>(a, s);
+        return backward<256, 1, true>(a, s);
     if (runs <= 512)
-        return backward<512, 1>(a, s);
+        return backward<512, 1, true>(a, s);
     if (runs <= 1024)
-        return backward<1024, 1>(a, s);
+        return backward<512, 2, true>(a, s);
     if (runs <= 2048)
-        return backward<1024, 2>(a, s);
-    return backward<1024, 4>(a, s);
+        return backward<1024, 2, false>(a, s);
+    return backward<1024, 4, false>(a, s);
 }
 
 }  // namespace qll
