@@ -748,8 +748,8 @@ def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=Tr
     bf = torch.bfloat16
     pA, pB = _arg(A, "A", bf, (M, K), here), _arg(B, "B", bf, (N, K), here)
     pd, pb = _arg(dout, "dout", bf, (M, N), here), _arg(bias, "bias", bf, (N,), here)
-    dA = (A.new_empty((M, K)) if dA is None else dA) if need_input else None
-    dB = (A.new_empty((N, K)) if dB is None else dB) if need_weight else None
+    dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
+    dB = (torch.empty_like(B) if dB is None else dB) if need_weight else None
     if bias is None:
         dbias = None
     elif dbias is None:
@@ -817,12 +817,13 @@ def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weigh
     if not (need_input or need_weight):
         raise ValueError("nothing to compute")
     L = load_library()
-    bf = _torch().bfloat16
+    torch = _torch()
+    bf = torch.bfloat16
     lead = (_arg(A, "A", bf, (M, K), here), _arg(Bg, "Bg", bf, (N, K), here),
             _arg(Bu, "Bu", bf, (N, K), here), _arg(dout, "dout", bf, (M, N), here), _act(act))
-    dA = (A.new_empty((M, K)) if dA is None else dA) if need_input else None
-    dBg = (A.new_empty((N, K)) if dBg is None else dBg) if need_weight else None
-    dBu = (A.new_empty((N, K)) if dBu is None else dBu) if need_weight else None
+    dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
+    dBg = (torch.empty_like(Bg) if dBg is None else dBg) if need_weight else None
+    dBu = (torch.empty_like(Bu) if dBu is None else dBu) if need_weight else None
     ws, wsb, keep = _scratch("qll_gated_backward_workspace_bytes",
                              L.qll_gated_backward_workspace_bytes(M, N, K), workspace, A, here)
     rc = L.gated_bf16_backward(
@@ -875,7 +876,7 @@ def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=
         ph = _arg(r_out, "r_out", dt, (M, K), here)
     if quantize:
         if n_out is None:
-            n_out = r.new_empty((M, K), dtype=torch.float8_e4m3fn)
+            n_out = torch.empty_like(r, dtype=torch.float8_e4m3fn)
         if scales is None:
             scales = r.new_empty((M, 1), dtype=torch.float32)
         pn, ps = _codes(n_out, "n_out", (M, K), here), _scales(scales, "scales", M, here)
@@ -883,7 +884,7 @@ def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=
         if scales is not None:
             raise ValueError("scales need quantize")
         if n_out is None:
-            n_out = r.new_empty((M, K), dtype=torch.bfloat16)
+            n_out = torch.empty_like(r, dtype=torch.bfloat16)
         pn, ps = _arg(n_out, "n_out", torch.bfloat16, (M, K), here), None
     rc = load_library().residual_norm(*lead, ph, pn, ps, M, K, st)
     if rc:

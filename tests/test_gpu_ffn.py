@@ -235,6 +235,28 @@ def test_residual_in_place(qll):
         assert got is res and torch.equal(got, want)
 
 
+def test_offsets_past_32_bits(qll):
+    """An output of more than 2^31 elements, and gradients whose operand spans
+    more than 2^31 bytes along the contraction; checked on rows at both ends."""
+    g = gen(8)
+    M, N, K = 66000, 33000, 16
+    x, w = rnd(g, M, K), rnd(g, N, K)
+    out = qll.gemm_bf16_epilogue(x, w, act="silu")
+    rows = torch.tensor([0, 1, 65063, 65075, 65999], device="cuda")
+    check(out[rows], ref.linear(x[rows].to(D), w.to(D), act="silu"), "out")
+    del out
+    M, N, K = 66000, 17000, 2568
+    x, w, d = rnd(g, M, K), rnd(g, N, K, std=0.05), rnd(g, M, N, std=0.1)
+    dA, dB, _ = qll.gemm_bf16_epilogue_backward(x, w, d)
+    cols = torch.tensor([0, 8191, 16383, 16999], device="cuda")
+    want = d[:, cols].to(D).t() @ x.to(D)
+    mag = d[:, cols].to(D).abs().t() @ x.to(D).abs()
+    check(dB[cols], (want, ref.gamma(M) * mag + ref.rounding(want, "bf16")), "dB")
+    rows = torch.tensor([0, 33000, 63161, 63170, 65999], device="cuda")
+    want, mag = d[rows].to(D) @ w.to(D), d[rows].to(D).abs() @ w.to(D).abs()
+    check(dA[rows], (want, ref.gamma(N) * mag + ref.rounding(want, "bf16")), "dA")
+
+
 NORM_SIZES = [(1, 16), (1, 4096), (3, 512), (2, 528), (7, 2048), (5, 2064), (3, 4112), (130, 8192),
               (4, 8208), (2, 16384), (3, 32768), (1030, 1040), (1030, 4096), (1025, 6160)]
 
