@@ -108,8 +108,16 @@ struct FfnSource {
     }
 };
 
+// The two slots, one object for every product of a kernel.
+__device__ __forceinline__ uint8_t* ffn_alt_ring()
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * 512 * 128];
+    return ring;
+}
+
+// Tiles first, first + step, ... of one product.
 template <bool FP8, int LAY, int EPI>
-__global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
+__device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int step)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
     using Copies = FfnCopies<FP8, LAY, DUAL, 256, 256, 4, 2>;
@@ -118,7 +126,7 @@ __global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
     constexpr bool PSTR = Copies::PSTR, QSTR = Copies::QSTR;
     constexpr bool SEGS = LAY == LAY_NN;
     constexpr int SLOT = Copies::SLOT;
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * SLOT];
+    uint8_t* const ring = ffn_alt_ring();
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -161,16 +169,15 @@ __global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
         }
         src_q.next(ldq, r0, cp.chq);
     };
-    // copy i (of 2) of a half
+    // copy i (of 2) of a half; `to`: where this wave's 1 KiB of a copy go
+    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring + wave * 1024);
     auto copy_p = [&](int h, int i, uint8_t* slot) __attribute__((always_inline)) {
         dma16(src_p[DUAL ? h : 0].v + cp.shift_p(h, i), src_p[DUAL ? h : 0].rs,
-              __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
-                  slot + h * SP::HB + (i * 8 + wave) * 1024)));
+              to + (uint32_t)(slot - ring) + h * SP::HB + i * 8192);
     };
     auto copy_q = [&](int h, int i, uint8_t* slot) __attribute__((always_inline)) {
         dma16(src_q.v + cp.shift_q(h, i), src_q.rs,
-              __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
-                  slot + 2 * SP::HB + h * SQ::HB + (i * 8 + wave) * 1024)));
+              to + (uint32_t)(slot - ring) + 2 * SP::HB + h * SQ::HB + i * 8192);
     };
 
     uint4 fp[2][SP::NB][2], fq[SQ::NB][2];
@@ -249,8 +256,10 @@ __global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
     };
 
     const int tiles = tr * tc;
-    start(blockIdx.x);
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    if (first >= tiles)
+        return;
+    start(first);
+    for (int t = first; t < tiles; t += step) {
         const int rt = r0, ct = c0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -280,10 +289,33 @@ __global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
         // next tile's first stages travel while this one's epilogue runs.
         wait_vm_barrier<0>();
         __builtin_amdgcn_sched_barrier(0);
-        if (t + gridDim.x < tiles)
-            start(t + gridDim.x);
+        if (t + step < tiles)
+            start(t + step);
         ffn_finish<SP, SQ, DUAL, EPI>(a, acc, ct, rt, rt / 256, wp, wq, 2, lane);
     }
+}
+
+template <bool FP8, int LAY, int EPI>
+__global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
+{
+    ffn_alt_tiles<FP8, LAY, EPI>(a, blockIdx.x, gridDim.x);
+}
+
+// Two products in one launch, the input's and the weights' gradients of a
+// backward pass: their tiles are numbered one after the other, so that they
+// fill the compute units together where neither does alone.  (Template only
+// so that every unit that includes this may define it.)
+template <int LAY_A, int LAY_B>
+__global__ __launch_bounds__(512, 2) void ffn_alt_pair_kernel(FfnArgs a, FfnArgs b)
+{
+    const int tiles_a = ((a.R + 255) / 256) * ((a.C + 255) / 256);
+    const int G = gridDim.x;
+    ffn_alt_tiles<false, LAY_A, EPI_PLAIN>(a, blockIdx.x, G);
+    // the first tile of b whose number, after a's, is this workgroup's
+    const int skip = tiles_a % G;
+    const int first = (int)blockIdx.x - skip;
+    __syncthreads();
+    ffn_alt_tiles<false, LAY_B, EPI_PLAIN>(b, first < 0 ? first + G : first, G);
 }
 
 }  // namespace qll

@@ -164,8 +164,8 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int act, bool bias, 
 int64_t split_offset(const BackwardPlan& p, int64_t N) { return p.strips + round256(p.nstrips * N * 4); }
 
 // dA [M][K] = dz B, over one (dz, B) or two segments side by side in dz.
-hipError_t input_gradient(const void* dz, const void* B0, const void* B1, void* dA, int64_t M,
-                          int64_t N, int64_t K, int splits, float* partial, hipStream_t stream)
+FfnArgs input_gradient(const void* dz, const void* B0, const void* B1, void* dA, int64_t M,
+                       int64_t N, int64_t K, int splits, float* partial)
 {
     FfnArgs a = blank();
     const int nseg = B1 ? 2 : 1;
@@ -187,13 +187,12 @@ hipError_t input_gradient(const void* dz, const void* B0, const void* B1, void* 
     a.partial = partial;
     a.out = dA;
     a.ldo = K;
-    return ffn_launch(0, LAY_NN, EPI_PLAIN, a, stream);
+    return a;
 }
 
 // dB [width][K] = dz^T A; rows from row_split on go to dB1.
-hipError_t weight_gradient(const void* dz, const void* A, void* dB0, void* dB1, int64_t row_split,
-                           int64_t M, int64_t width, int64_t K, int splits, float* partial,
-                           hipStream_t stream)
+FfnArgs weight_gradient(const void* dz, const void* A, void* dB0, void* dB1, int64_t row_split,
+                        int64_t M, int64_t width, int64_t K, int splits, float* partial)
 {
     FfnArgs a = blank();
     a.P[0] = a.P[1] = (const uint8_t*)A;
@@ -212,7 +211,20 @@ hipError_t weight_gradient(const void* dz, const void* A, void* dB0, void* dB1, 
     a.out2 = dB1;
     a.row_split = (int)row_split;
     a.ldo = K;
-    return ffn_launch(0, LAY_TN, EPI_PLAIN, a, stream);
+    return a;
+}
+
+// Either gradient, or both, in one launch where that pays.
+hipError_t run_gradients(const FfnArgs* in, const FfnArgs* w, hipStream_t stream)
+{
+    if (in && w && ffn_pair_fits(*in, *w))
+        return ffn_launch_pair(*in, *w, stream);
+    hipError_t e = hipSuccess;
+    if (in)
+        e = ffn_launch(0, LAY_NN, EPI_PLAIN, *in, stream);
+    if (w && e == hipSuccess)
+        e = ffn_launch(0, LAY_TN, EPI_PLAIN, *w, stream);
+    return e;
 }
 
 int validate_backward(int64_t M, int64_t N, int64_t K, int act)
@@ -312,12 +324,9 @@ int gemm_bf16_epilogue_backward(const void* A, const void* B, const void* dout, 
         if (launch_colsum_finish(c, 1, s) != hipSuccess)
             return QLL_ERR_HIP;
     }
-    if (dA && M > 0 &&
-        input_gradient(dz, B, nullptr, dA, M, N, K, p.splits_in, pieces, s) != hipSuccess)
-        return QLL_ERR_HIP;
-    if (dB && weight_gradient(dz, A, dB, nullptr, 0x7FFFFFFF, M, N, K, p.splits_w, pieces, s) != hipSuccess)
-        return QLL_ERR_HIP;
-    return QLL_OK;
+    const FfnArgs in = input_gradient(dz, B, nullptr, dA, M, N, K, p.splits_in, pieces);
+    const FfnArgs wt = weight_gradient(dz, A, dB, nullptr, 0x7FFFFFFF, M, N, K, p.splits_w, pieces);
+    return hip_status(run_gradients(dA && M > 0 ? &in : nullptr, dB ? &wt : nullptr, s));
 }
 
 int gated_bf16(const void* A, const void* Bg, const void* Bu, int act, void* out, int out_dtype,
@@ -375,12 +384,9 @@ int gated_bf16_backward(const void* A, const void* Bg, const void* Bu, const voi
         if (ffn_launch(0, LAY_NT, EPI_DGATED, a, s) != hipSuccess)
             return QLL_ERR_HIP;
     }
-    if (dA && M > 0 &&
-        input_gradient(w + p.dz, Bg, Bu, dA, M, N, K, p.splits_in, pieces, s) != hipSuccess)
-        return QLL_ERR_HIP;
-    if (dBg && weight_gradient(w + p.dz, A, dBg, dBu, N, M, 2 * N, K, p.splits_w, pieces, s) != hipSuccess)
-        return QLL_ERR_HIP;
-    return QLL_OK;
+    const FfnArgs in = input_gradient(w + p.dz, Bg, Bu, dA, M, N, K, p.splits_in, pieces);
+    const FfnArgs wt = weight_gradient(w + p.dz, A, dBg, dBu, N, M, 2 * N, K, p.splits_w, pieces);
+    return hip_status(run_gradients(dA && M > 0 ? &in : nullptr, dBg ? &wt : nullptr, s));
 }
 
 namespace {

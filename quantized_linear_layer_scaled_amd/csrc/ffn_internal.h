@@ -69,6 +69,10 @@ int ffn_dz_strips(int64_t R, int64_t C);
 int ffn_splits(int64_t R, int64_t C, int64_t stages);
 
 hipError_t ffn_launch(int fp8, int layout, int epi, FfnArgs a, hipStream_t stream);
+// The input's (LAY_NN) and the weights' (LAY_TN) gradient in one launch,
+// where ffn_pair_fits.
+bool ffn_pair_fits(const FfnArgs& in, const FfnArgs& w);
+hipError_t ffn_launch_pair(const FfnArgs& in, const FfnArgs& w, hipStream_t stream);
 // Sum of the Split-K pieces followed by EPI_LINEAR.
 hipError_t ffn_launch_reduce(const FfnArgs& a, hipStream_t stream);
 // Few rows (R <= kFfnSkinnyRows): one pass over the weights, K split over the

@@ -104,9 +104,11 @@ GRAD_SIZES = [(1, 64, 128), (1, 8, 8), (5, 24, 40), (64, 72, 136), (65, 136, 72)
               (257, 520, 264), (300, 1032, 512), (1025, 264, 136), (2100, 1304, 264), (4096, 64, 64),
               # the 256x256 tile in one of the products each
               (4100, 72, 4360), (72, 4104, 4360), (4100, 4360, 72), (4100, 4360, 200)]
+# both gradients in one launch
+PAIR_SIZES = [(4100, 4104, 2056), (4100, 2056, 2056), (2000, 2304, 4360)]
 
 
-@pytest.mark.parametrize("M,N,K", GRAD_SIZES)
+@pytest.mark.parametrize("M,N,K", GRAD_SIZES + PAIR_SIZES)
 @pytest.mark.parametrize("act", ["none", "gelu", "silu"])
 def test_linear_backward(qll, act, M, N, K):
     g = gen(M + N + K)
@@ -137,7 +139,7 @@ def test_backward_of_every_activation(qll, act):
         check(t, r, act)
 
 
-@pytest.mark.parametrize("M,N,K", GRAD_SIZES)
+@pytest.mark.parametrize("M,N,K", GRAD_SIZES + PAIR_SIZES)
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_gated_backward(qll, act, M, N, K):
     g = gen(M + N + K)
