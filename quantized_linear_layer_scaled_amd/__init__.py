@@ -603,11 +603,9 @@ def _refuse(t, name, what, here):
     raise ValueError(f"{name} must be {what}")
 
 
-def _arg(t, name, dtype, shape, here):
+def _need(t, name, dtype, shape, here):
     """Pointer of a contiguous tensor of this type and shape on the current
-    device; None for None."""
-    if t is None:
-        return None
+    device."""
     try:
         if (t.dtype is dtype and t.shape == shape and t.get_device() == here and
                 t.is_contiguous()):
@@ -617,31 +615,33 @@ def _arg(t, name, dtype, shape, here):
     _refuse(t, name, f"{dtype} of shape {tuple(shape)}", here)
 
 
+def _arg(t, name, dtype, shape, here):
+    """The same, None for None."""
+    return None if t is None else _need(t, name, dtype, shape, here)
+
+
 def _codes(t, name, shape, here):
     """Pointer of e4m3 codes: float8_e4m3fn, or their bytes."""
     torch = _torch()
     dt = getattr(t, "dtype", None)
-    if dt is torch.uint8 or dt is torch.int8:
-        return _arg(t, name, dt, shape, here)
-    return _arg(t, name, torch.float8_e4m3fn, shape, here)
+    if dt is not torch.uint8 and dt is not torch.int8:
+        dt = torch.float8_e4m3fn
+    return _need(t, name, dt, shape, here)
 
 
 def _scales(t, name, n, here):
     """Pointer of n fp32 scales, [n] or [n][1]."""
-    shape = (n, 1) if getattr(t, "ndim", 1) == 2 else (n,)
-    return _arg(t, name, _torch().float32, shape, here)
-
-
-def _required(**tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise TypeError(f"{name} must be a torch tensor")
+    return _need(t, name, _torch().float32,
+                 (n, 1) if getattr(t, "ndim", 1) == 2 else (n,), here)
 
 
 def _matrix(t, name):
-    if getattr(t, "ndim", None) != 2:
+    shape = getattr(t, "shape", None)
+    if shape is None:
+        raise TypeError(f"{name} must be a torch tensor")
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    return t.shape
+    return shape
 
 
 def _act(act):
@@ -683,7 +683,6 @@ def _scratch(query, need, workspace, like, here):
 def _epilogue(fp8, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace):
     torch = _torch()
     here, st = _place()
-    _required(A=A, B=B)
     M, K = _matrix(A, "A")
     N = _matrix(B, "B")[0]
     bf = torch.bfloat16
@@ -691,12 +690,11 @@ def _epilogue(fp8, A, B, sa, sb, bias, residual, act, out_dtype, out, workspace)
     pb, pr = _arg(bias, "bias", bf, (N,), here), _arg(residual, "residual", bf, (M, N), here)
     code = _act(act)
     if fp8:
-        _required(sa=sa, sb=sb)
         lead = (_codes(A, "A", (M, K), here), _codes(B, "B", (N, K), here),
                 _scales(sa, "sa", M, here), _scales(sb, "sb", N, here))
         fn, f = "gemm_fp8_epilogue", L.gemm_fp8_epilogue
     else:
-        lead = (_arg(A, "A", bf, (M, K), here), _arg(B, "B", bf, (N, K), here))
+        lead = (_need(A, "A", bf, (M, K), here), _need(B, "B", bf, (N, K), here))
         fn, f = "gemm_bf16_epilogue", L.gemm_bf16_epilogue
     out, po, od = _float_out(out, M, N, out_dtype, A, here)
     ws, wsb, keep = _scratch("qll_epilogue_workspace_bytes",
@@ -738,7 +736,6 @@ def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=Tr
                       need_weight, dA, dB, dbias, workspace)
     torch = _torch()
     here, st = _place()
-    _required(A=A, B=B, dout=dout)
     M, K = _matrix(A, "A")
     N = _matrix(B, "B")[0]
     code = _act(act)
@@ -746,8 +743,8 @@ def gemm_bf16_epilogue_backward(A, B, dout, bias=None, act="none", need_input=Tr
         raise ValueError("nothing to compute")
     L = load_library()
     bf = torch.bfloat16
-    pA, pB = _arg(A, "A", bf, (M, K), here), _arg(B, "B", bf, (N, K), here)
-    pd, pb = _arg(dout, "dout", bf, (M, N), here), _arg(bias, "bias", bf, (N,), here)
+    pA, pB = _need(A, "A", bf, (M, K), here), _need(B, "B", bf, (N, K), here)
+    pd, pb = _need(dout, "dout", bf, (M, N), here), _arg(bias, "bias", bf, (N,), here)
     dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
     dB = (torch.empty_like(B) if dB is None else dB) if need_weight else None
     if bias is None:
@@ -770,12 +767,11 @@ def gated_bf16(A, Bg, Bu, act="silu", out_dtype="bf16", out=None, stream=None):
     if stream is not None:
         return _under(stream, gated_bf16, A, Bg, Bu, act, out_dtype, out)
     here, st = _place()
-    _required(A=A, Bg=Bg, Bu=Bu)
     M, K = _matrix(A, "A")
     N = _matrix(Bg, "Bg")[0]
     bf = _torch().bfloat16
-    pA, pg = _arg(A, "A", bf, (M, K), here), _arg(Bg, "Bg", bf, (N, K), here)
-    pu = _arg(Bu, "Bu", bf, (N, K), here)
+    pA, pg = _need(A, "A", bf, (M, K), here), _need(Bg, "Bg", bf, (N, K), here)
+    pu = _need(Bu, "Bu", bf, (N, K), here)
     code = _act(act)
     out, po, od = _float_out(out, M, N, out_dtype, A, here)
     rc = load_library().gated_bf16(pA, pg, pu, code, po, od, M, N, K, st)
@@ -790,7 +786,6 @@ def gated_fp8(A, Bg, Bu, sa, sg, su, act="silu", out_dtype="bf16", out=None, str
     if stream is not None:
         return _under(stream, gated_fp8, A, Bg, Bu, sa, sg, su, act, out_dtype, out)
     here, st = _place()
-    _required(A=A, Bg=Bg, Bu=Bu, sa=sa, sg=sg, su=su)
     M, K = _matrix(A, "A")
     N = _matrix(Bg, "Bg")[0]
     lead = (_codes(A, "A", (M, K), here), _codes(Bg, "Bg", (N, K), here),
@@ -811,7 +806,6 @@ def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weigh
         return _under(stream, gated_bf16_backward, A, Bg, Bu, dout, act, need_input, need_weight,
                       dA, dBg, dBu, workspace)
     here, st = _place()
-    _required(A=A, Bg=Bg, Bu=Bu, dout=dout)
     M, K = _matrix(A, "A")
     N = _matrix(Bg, "Bg")[0]
     if not (need_input or need_weight):
@@ -819,8 +813,8 @@ def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weigh
     L = load_library()
     torch = _torch()
     bf = torch.bfloat16
-    lead = (_arg(A, "A", bf, (M, K), here), _arg(Bg, "Bg", bf, (N, K), here),
-            _arg(Bu, "Bu", bf, (N, K), here), _arg(dout, "dout", bf, (M, N), here), _act(act))
+    lead = (_need(A, "A", bf, (M, K), here), _need(Bg, "Bg", bf, (N, K), here),
+            _need(Bu, "Bu", bf, (N, K), here), _need(dout, "dout", bf, (M, N), here), _act(act))
     dA = (torch.empty_like(A) if dA is None else dA) if need_input else None
     dBg = (torch.empty_like(Bg) if dBg is None else dBg) if need_weight else None
     dBu = (torch.empty_like(Bu) if dBu is None else dBu) if need_weight else None
@@ -837,7 +831,6 @@ def gated_bf16_backward(A, Bg, Bu, dout, act="silu", need_input=True, need_weigh
 def _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here):
     torch = _torch()
     bf = torch.bfloat16
-    _required(r=r, w_pre=w_pre)
     M, K = _matrix(r, "r")
     dt = r.dtype
     if dt is bf:
@@ -848,9 +841,9 @@ def _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here):
         raise ValueError("r must be bfloat16 or float32")
     if y is None and (w_post is not None or gate is not None or alpha != 1.0):
         raise ValueError("w_post, gate and alpha need a block output y")
-    return M, K, dt, (_arg(y, "y", bf, (M, K), here), _arg(r, "r", dt, (M, K), here), kind,
+    return M, K, dt, (_arg(y, "y", bf, (M, K), here), _need(r, "r", dt, (M, K), here), kind,
                       _arg(w_post, "w_post", bf, (K,), here), _arg(gate, "gate", bf, (K,), here),
-                      _arg(w_pre, "w_pre", bf, (K,), here), alpha, beta, eps)
+                      _need(w_pre, "w_pre", bf, (K,), here), alpha, beta, eps)
 
 
 def residual_norm(y, r, w_pre, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
@@ -905,7 +898,6 @@ def residual_norm_backward(y, r, w_pre, dn, dr_out=None, w_post=None, gate=None,
     torch = _torch()
     here, st = _place()
     M, K, dt, lead = _norm_args(y, r, w_pre, w_post, gate, alpha, beta, eps, here)
-    _required(dn=dn)
     L = load_library()
     bf, f32 = torch.bfloat16, torch.float32
     if y is None:
@@ -927,7 +919,7 @@ def residual_norm_backward(y, r, w_pre, dn, dr_out=None, w_post=None, gate=None,
     ws, wsb, keep = _scratch("qll_residual_norm_backward_workspace_bytes",
                              L.qll_residual_norm_backward_workspace_bytes(M, K), workspace, r, here)
     rc = L.residual_norm_backward(
-        *lead, _arg(dn, "dn", bf, (M, K), here), _arg(dr_out, "dr_out", dt, (M, K), here),
+        *lead, _need(dn, "dn", bf, (M, K), here), _arg(dr_out, "dr_out", dt, (M, K), here),
         _arg(dy, "dy", bf, (M, K), here), _arg(dr, "dr", dt, (M, K), here),
         _arg(dw_post, "dw_post", f32, (K,), here), _arg(dgate, "dgate", f32, (K,), here),
         _arg(dw_pre, "dw_pre", f32, (K,), here), M, K, ws, wsb, st)

@@ -487,6 +487,13 @@ def test_refusals(qll):
     assert e.value.status == 4
     with pytest.raises(ValueError):
         qll.gated_bf16(x, w, rnd(g, 16, 64))
+    for bad in (lambda: qll.gemm_bf16_epilogue(None, w), lambda: qll.gemm_bf16_epilogue(x, None),
+                lambda: qll.gated_bf16(x, w, None), lambda: qll.gated_bf16_backward(x, w, w, None),
+                lambda: qll.gemm_fp8_epilogue(*quant(x)[:1], *quant(w)[:1], None, quant(w)[1]),
+                lambda: qll.residual_norm(x, None, b), lambda: qll.residual_norm(x, x, None),
+                lambda: qll.residual_norm_backward(x, x, rnd(g, 64), None)):
+        with pytest.raises(TypeError):
+            bad()
     with pytest.raises(ValueError):
         qll.residual_norm(None, x, rnd(g, 64), gate=rnd(g, 64))
     with pytest.raises(ValueError):
