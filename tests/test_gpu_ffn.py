@@ -440,6 +440,51 @@ def test_train_step_in_a_graph(qll):
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
 
 
+def test_serving_calls_in_a_graph(qll):
+    """FP8 serving calls of several kernels, Split-K among them, captured with
+    outputs and workspace of the caller's; replays after both were overwritten
+    give the eager bits."""
+    H, F = 256, 16384
+    s = block_state(80, H, H, 7)
+    g = gen(8)
+    (gq, sg), (uq, su) = quant(rnd(g, F, H, std=0.05)), quant(rnd(g, F, H, std=0.05))
+    dq, sd = quant(rnd(g, H, F, std=0.05))
+    L = qll.load_library()
+    for M in (1, 16, 80):
+        y, r = s["y"][:M].contiguous(), s["r"][:M].contiguous()
+        n = torch.empty(M, H, dtype=torch.float8_e4m3fn, device="cuda")
+        sc, h = torch.empty(M, 1, device="cuda"), torch.empty_like(r)
+        a, out = torch.empty(M, F, dtype=BF, device="cuda"), torch.empty(M, H, dtype=F32, device="cuda")
+        aq, sa = torch.empty(M, F, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(M, 1, device="cuda")
+        need = L.qll_epilogue_workspace_bytes(1, M, H, F)
+        assert (need > 0) == (M == 80)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+
+        def step():
+            qll.residual_norm(y, r, s["w2"], w_post=s["w1"], quantize=True, r_out=h, n_out=n, scales=sc)
+            qll.gated_fp8(n, gq, uq, sc, sg, su, out=a)
+            qll.quantize_per_token_fp8(a, q=aq, scales=sa)
+            qll.gemm_fp8_epilogue(aq, dq, sa, sd, residual=h, act="gelu", out_dtype="fp32", out=out, workspace=ws)
+
+        step()
+        want = [t.clone() for t in (h, a, out)]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for _ in range(3):
+            for t in (h, a, out):
+                t.fill_(3.0)
+            ws.fill_(0x5A)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(t, w) for t, w in zip((h, a, out), want))
+
+
 def test_repeatable_and_on_other_streams(qll):
     s = block_state(700, 512, 1032, 5)
     dout = rnd(gen(6), 700, 512)
