@@ -61,8 +61,8 @@ enum FfnLayout : int {
     LAY_TN       // both K-strided (gradient of the weights)
 };
 
-// Rows of R that one row of the EPI_DZ column sums covers, for the tile the
-// launch picks for (R, C).
+// Rows of `partial` that EPI_DZ writes: strips of rows whose column sums it
+// forms, for the tile the launch picks for (R, C).
 int ffn_dz_strips(int64_t R, int64_t C);
 // Split-K pieces that the launch of a bf16 input-gradient or linear product
 // uses for (R, C, stages), 1 = none.
