@@ -48,66 +48,6 @@
 
 namespace qll {
 
-// One operand's source of the copies of a tile: its resource and this lane's
-// offset at the stage being copied.  A K-contiguous operand keeps its resource
-// (the tile's rows) and moves the offset; past the end of K the offset is out
-// of range.  A K-strided one keeps the offset and moves the resource by 64 k
-// lines; it ends where the matrix does.  All of it is 32-bit arithmetic once
-// per stage, so that a copy is one addition and the load.
-template <bool STR>
-struct FfnSource {
-    v4i rs;
-    uint32_t v;
-    int lines;  // strided: k lines from the stage to the end of the matrix
-    int kleft;  // contiguous: bytes of K from the stage to the end
-
-    // tile corner at row (column) x0 of `extent`; ch: this lane's chunk
-    __device__ __forceinline__ void set(const uint8_t* base, uint32_t ld, int x0, int extent,
-                                        int klen, int esz, uint32_t v0, int ch)
-    {
-        v = v0;
-        if constexpr (STR) {
-            const uint64_t at = (uint64_t)(uintptr_t)base + 2 * (int64_t)x0;
-            rs.x = (int)(uint32_t)at;
-            rs.y = (int)(uint32_t)(at >> 32) & 0xFFFF;
-            rs.w = 0x00020000;
-            lines = klen;
-            limit(ld, x0);
-        } else {
-            // (offsets stay below 256 rows, a row past `extent` is out of range)
-            const int rows = min(extent - x0, 256);
-            rs = buffer_rsrc(base + (int64_t)x0 * ld, (uint32_t)rows * ld);
-            kleft = klen * esz;
-            clip(ch);
-        }
-    }
-    __device__ __forceinline__ void limit(uint32_t ld, int x0)
-    {
-        // (one stage reads 64 lines: the last of them may end the matrix)
-        const int n = max(min(lines, 64), 0) * (int)ld - 2 * x0;
-        rs.z = __builtin_amdgcn_readfirstlane(max(n, 0));
-    }
-    __device__ __forceinline__ void clip(int ch)
-    {
-        if (kleft < 128 && ch * 16 >= kleft)
-            v = kOutOfRange;
-    }
-    __device__ __forceinline__ void next(uint32_t ld, int x0, int ch)
-    {
-        if constexpr (STR) {
-            const uint64_t at = (((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x) + 64ull * ld;
-            rs.x = (int)(uint32_t)at;
-            rs.y = (int)(uint32_t)(at >> 32);
-            lines -= 64;
-            limit(ld, x0);
-        } else {
-            v += 128;
-            kleft -= 128;
-            clip(ch);
-        }
-    }
-};
-
 // The two slots, one object for every product of a kernel.
 __device__ __forceinline__ uint8_t* ffn_alt_ring()
 {

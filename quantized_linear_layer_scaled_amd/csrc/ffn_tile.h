@@ -27,8 +27,9 @@
 // Copies go from global memory to LDS directly (buffer_load_dwordx4 ... lds)
 // through resources that end where the matrix ends: rows past the end, and K
 // past the end of a strided operand, read as zeros; K past the end of a
-// contiguous row gets an offset out of range.  Resources are rebuilt per
-// stage from 64-bit addresses, so no operand size overflows 32-bit offsets.
+// contiguous row gets an offset out of range.  No operand size overflows the
+// 32-bit offsets: a contiguous operand's cover 256 rows, a strided one's 64 k
+// lines from a 64-bit base that moves on with the stages.
 #pragma once
 
 #include "ffn_epilogue.h"
@@ -96,14 +97,6 @@ template <typename S, bool SPLIT>
 __device__ __forceinline__ int ffn_tile_row(int h, int r)
 {
     return SPLIT ? (r / S::SH) * 2 * S::SH + h * S::SH + r % S::SH : h * S::H + r;
-}
-
-// Resource of `base` from byte `off` to byte `avail` (none left: reads zeros).
-__device__ __forceinline__ v4i ffn_rsrc(const uint8_t* base, int64_t off, int64_t avail)
-{
-    const int64_t left = avail - off;
-    return buffer_rsrc(base + (left > 0 ? off : 0),
-                       (uint32_t)(left <= 0 ? 0 : (left < 0x7FFFFFFF ? left : 0x7FFFFFFF)));
 }
 
 template <bool FP8>
@@ -222,8 +215,8 @@ __device__ __forceinline__ void ffn_finish(const FfnArgs& a, v4f (&acc)[2][SP::N
         with_act(a.act, run);
 }
 
-// A wave's copies of one tile: per-lane source offsets relative to the tile's
-// corner, and the copies of one half of one operand at stage kt.
+// A wave's copies of a tile: per-lane source offsets relative to the tile's
+// corner.
 template <bool FP8, int LAY, bool DUAL, int BP, int BQ, int WP, int WQ>
 struct FfnCopies {
     static constexpr int WAVES = WP * WQ;
@@ -234,8 +227,6 @@ struct FfnCopies {
     static constexpr int SLOT = (BP + BQ) * 128;
 
     const FfnArgs& a;
-    int wave;
-    uint32_t kbytes;
     // the source offsets of copy 0 of half 0; the others differ by the same
     // scalar in every lane
     uint32_t vp, vq;
@@ -246,13 +237,13 @@ struct FfnCopies {
                   "copies of a half repeat the swizzle");
 
     __device__ __forceinline__ FfnCopies(const FfnArgs& args, int w, int lane)
-        : a(args), wave(w), kbytes((uint32_t)args.klen * (FP8 ? 1 : 2))
+        : a(args)
     {
         int line;
-        SP::source(0, wave, lane, line, chp);
+        SP::source(0, w, lane, line, chp);
         vp = PSTR ? (uint32_t)line * (uint32_t)a.ldp + 2 * ffn_tile_row<SP, !DUAL>(0, chp * 8)
                   : (uint32_t)ffn_tile_row<SP, !DUAL>(0, line) * (uint32_t)a.ldp + chp * 16;
-        SQ::source(0, wave, lane, line, chq);
+        SQ::source(0, w, lane, line, chq);
         vq = QSTR ? (uint32_t)line * (uint32_t)a.ldq + 2 * ffn_tile_row<SQ, false>(0, chq * 8)
                   : (uint32_t)ffn_tile_row<SQ, false>(0, line) * (uint32_t)a.ldq + chq * 16;
     }
@@ -268,54 +259,101 @@ struct FfnCopies {
         return QSTR ? (uint32_t)(i * LINES_Q) * (uint32_t)a.ldq + 2 * ffn_tile_row<SQ, false>(h, 0)
                     : (uint32_t)ffn_tile_row<SQ, false>(h, i * LINES_Q) * (uint32_t)a.ldq;
     }
-    __device__ __forceinline__ void copy_p(int h, int kt, int c0, uint8_t* slot) const
+};
+
+// One operand's source of the copies of a tile: its resource and this lane's
+// offset at the stage being copied.  A K-contiguous operand keeps its resource
+// (the tile's rows) and moves the offset; past the end of K the offset is out
+// of range.  A K-strided one keeps the offset and moves the resource by 64 k
+// lines; it ends where the matrix does.  All of it is 32-bit arithmetic once
+// per stage, so that a copy is one addition and the load.
+template <bool STR>
+struct FfnSource {
+    v4i rs;
+    uint32_t v;
+    int lines;  // strided: k lines from the stage to the end of the matrix
+    int kleft;  // contiguous: bytes of K from the stage to the end
+
+    // tile corner at row (column) x0 of `extent`; ch: this lane's chunk
+    __device__ __forceinline__ void set(const uint8_t* base, uint32_t ld, int x0, int extent,
+                                        int klen, int esz, uint32_t v0, int ch)
     {
-        const int seg = kt >= a.nks ? 1 : 0;
-        const int kk = kt - seg * a.nks;
-        const uint32_t kb = (uint32_t)kk * 128u;
-        const int src = DUAL ? h : seg;
-        const v4i rs = ffn_rsrc(a.P[src],
-                                PSTR ? (int64_t)kk * 64 * a.ldp + 2 * c0 : (int64_t)c0 * a.ldp + kb,
-                                a.availP[src]);
-#pragma unroll
-        for (int i = 0; i < SP::LD; ++i) {
-            uint32_t vo = vp + shift_p(h, i);
-            if (!PSTR && kb + 128 > kbytes && kb + chp * 16 >= kbytes)
-                vo = kOutOfRange;
-            dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
-                              slot + h * SP::HB + (i * WAVES + wave) * 1024)));
+        v = v0;
+        if constexpr (STR) {
+            const uint64_t at = (uint64_t)(uintptr_t)base + 2 * (int64_t)x0;
+            rs.x = (int)(uint32_t)at;
+            rs.y = (int)(uint32_t)(at >> 32) & 0xFFFF;
+            rs.w = 0x00020000;
+            lines = klen;
+            limit(ld, x0);
+        } else {
+            // (offsets stay below 256 rows, a row past `extent` is out of range)
+            const int rows = min(extent - x0, 256);
+            rs = buffer_rsrc(base + (int64_t)x0 * ld, (uint32_t)rows * ld);
+            kleft = klen * esz;
+            clip(ch);
         }
     }
-    __device__ __forceinline__ void copy_q(int h, int kt, int r0, uint8_t* slot) const
+    // on by n stages
+    __device__ __forceinline__ void skip(int n, uint32_t ld, int x0, int ch)
     {
-        const int seg = kt >= a.nks ? 1 : 0;
-        const int kk = kt - seg * a.nks;
-        const uint32_t kb = (uint32_t)kk * 128u;
-        const v4i rs = ffn_rsrc(a.Q[seg],
-                                QSTR ? (int64_t)kk * 64 * a.ldq + 2 * r0 : (int64_t)r0 * a.ldq + kb,
-                                a.availQ[seg]);
-#pragma unroll
-        for (int i = 0; i < SQ::LD; ++i) {
-            uint32_t vo = vq + shift_q(h, i);
-            if (!QSTR && kb + 128 > kbytes && kb + chq * 16 >= kbytes)
-                vo = kOutOfRange;
-            dma16(vo, rs, __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
-                              slot + 2 * SP::HB + h * SQ::HB + (i * WAVES + wave) * 1024)));
+        if constexpr (STR) {
+            const uint64_t at =
+                (((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x) + (uint64_t)n * 64u * ld;
+            rs.x = (int)(uint32_t)at;
+            rs.y = (int)(uint32_t)(at >> 32);
+            lines -= 64 * n;
+            limit(ld, x0);
+        } else {
+            v += 128u * (uint32_t)n;
+            kleft -= 128 * n;
+            clip(ch);
+        }
+    }
+    __device__ __forceinline__ void limit(uint32_t ld, int x0)
+    {
+        // (one stage reads 64 lines: the last of them may end the matrix)
+        const int n = max(min(lines, 64), 0) * (int)ld - 2 * x0;
+        rs.z = __builtin_amdgcn_readfirstlane(max(n, 0));
+    }
+    __device__ __forceinline__ void clip(int ch)
+    {
+        if (kleft < 128 && ch * 16 >= kleft)
+            v = kOutOfRange;
+    }
+    __device__ __forceinline__ void next(uint32_t ld, int x0, int ch)
+    {
+        if constexpr (STR) {
+            const uint64_t at = (((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x) + 64ull * ld;
+            rs.x = (int)(uint32_t)at;
+            rs.y = (int)(uint32_t)(at >> 32);
+            lines -= 64;
+            limit(ld, x0);
+        } else {
+            v += 128;
+            kleft -= 128;
+            clip(ch);
         }
     }
 };
 
-// Ring of S stages: every wave copies its share of stage kt + S - 1 while the
-// workgroup computes stage kt; one barrier per stage.
+// Ring of S stages.  At stage kt, once its fragments are in registers and
+// stage kt + 1 has landed (one barrier), the copies of stage kt + S go into the
+// slot of stage kt, the fragments of stage kt + 1 into the other register set,
+// and the products of stage kt run under both.  Two waves per SIMD, from one
+// workgroup of eight or two of four.
 template <bool FP8, int LAY, int EPI, int BP, int BQ, int WP, int WQ, int S>
-__global__ __launch_bounds__(WP* WQ * 64) void ffn_ring_kernel(FfnArgs a)
+__global__ __launch_bounds__(WP* WQ * 64, 2) void ffn_ring_kernel(FfnArgs a)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
     using Copies = FfnCopies<FP8, LAY, DUAL, BP, BQ, WP, WQ>;
     using SP = typename Copies::SP;
     using SQ = typename Copies::SQ;
+    constexpr bool PSTR = Copies::PSTR, QSTR = Copies::QSTR;
+    constexpr bool SEGS = LAY == LAY_NN;
     constexpr int SLOT = Copies::SLOT;
     constexpr int LPT = 2 * (SP::LD + SQ::LD);  // copies per wave and stage
+    constexpr int WAVES = WP * WQ;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * SLOT];
 
     const int lane = threadIdx.x & 63;
@@ -329,11 +367,44 @@ __global__ __launch_bounds__(WP* WQ * 64) void ffn_ring_kernel(FfnArgs a)
     const int kt0 = blockIdx.y * a.per;
     const int kt1 = min(a.nseg * a.nks, kt0 + a.per);
     const Copies cp(a, wave, lane);
-    auto issue = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
-        cp.copy_p(0, kt, c0, slot);
-        cp.copy_p(1, kt, c0, slot);
-        cp.copy_q(0, kt, r0, slot);
-        cp.copy_q(1, kt, r0, slot);
+
+    FfnSource<PSTR> src_p[DUAL ? 2 : 1];
+    FfnSource<QSTR> src_q;
+    const uint32_t ldp = (uint32_t)a.ldp, ldq = (uint32_t)a.ldq;
+    int left;  // stages of the segment from the next copies' on
+    auto seek = [&](int seg, int n) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < (DUAL ? 2 : 1); ++h) {
+            src_p[h].set(a.P[DUAL ? h : seg], ldp, c0, a.C, a.klen, FP8 ? 1 : 2, cp.vp, cp.chp);
+            src_p[h].skip(n, ldp, c0, cp.chp);
+        }
+        src_q.set(a.Q[seg], ldq, r0, a.R, a.klen, FP8 ? 1 : 2, cp.vq, cp.chq);
+        src_q.skip(n, ldq, r0, cp.chq);
+        left = a.nks - n;
+    };
+    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring + wave * 1024);
+    // this wave's copies of the next stage, into slot `s`
+    auto issue = [&](int s) __attribute__((always_inline)) {
+        const uint32_t at = to + (uint32_t)s * SLOT;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < SP::LD; ++i)
+                dma16(src_p[DUAL ? h : 0].v + cp.shift_p(h, i), src_p[DUAL ? h : 0].rs,
+                      at + h * SP::HB + i * (WAVES * 1024));
+#pragma unroll
+            for (int i = 0; i < SQ::LD; ++i)
+                dma16(src_q.v + cp.shift_q(h, i), src_q.rs,
+                      at + 2 * SP::HB + h * SQ::HB + i * (WAVES * 1024));
+        }
+        if (SEGS && --left == 0) {
+            seek(1, 0);
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < (DUAL ? 2 : 1); ++h)
+            src_p[h].next(ldp, c0, cp.chp);
+        src_q.next(ldq, r0, cp.chq);
     };
 
     v4f acc[2][SP::NB][2][SQ::NB];
@@ -347,39 +418,61 @@ __global__ __launch_bounds__(WP* WQ * 64) void ffn_ring_kernel(FfnArgs a)
                 for (int i = 0; i < SQ::NB; ++i)
                     acc[h][j][q][i] = v4f{0, 0, 0, 0};
 
+    uint4 fp[2][2][SP::NB][2], fq[2][2][SQ::NB][2];
+    auto read = [&](auto SET, int s) __attribute__((always_inline)) {
+        constexpr int set = decltype(SET)::value;
+        const uint8_t* sp = ring + s * SLOT;
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s)
-        if (kt0 + s < kt1)
-            issue(kt0 + s, ring + s * SLOT);
-    int slot = 0;
-    for (int kt = kt0; kt < kt1; ++kt) {
-        // stage kt has landed for every wave, and every wave is done reading
-        // the slot that the next copy overwrites
-        wait_younger<S - 2, LPT>(min(S - 2, kt1 - 1 - kt));
-        if (kt + S - 1 < kt1)
-            issue(kt + S - 1, ring + (slot == 0 ? S - 1 : slot - 1) * SLOT);
-        const uint8_t* sp = ring + slot * SLOT;
-        const uint8_t* sq = sp + 2 * SP::HB;
-        uint4 fp[2][SP::NB][2], fq[SQ::NB][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int j = 0; j < SP::NB; ++j)
-                ffn_frag<SP, Copies::PSTR>(sp + h * SP::HB, wp, j, lane, fp[h][j]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
+                ffn_frag<SP, PSTR>(sp + h * SP::HB, wp, j, lane, fp[set][h][j]);
 #pragma unroll
             for (int i = 0; i < SQ::NB; ++i)
-                ffn_frag<SQ, Copies::QSTR>(sq + q * SQ::HB, wq, i, lane, fq[i]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < SP::NB; ++j)
-#pragma unroll
-                    for (int i = 0; i < SQ::NB; ++i)
-                        acc[h][j][q][i] = ffn_mfma<FP8>(fp[h][j], fq[i], acc[h][j][q][i]);
+                ffn_frag<SQ, QSTR>(sp + 2 * SP::HB + h * SQ::HB, wq, i, lane, fq[set][h][i]);
         }
-        slot = slot + 1 == S ? 0 : slot + 1;
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    if (kt0 < kt1) {  // (the same for every wave)
+        if (SEGS && kt0 >= a.nks)
+            seek(1, kt0 - a.nks);
+        else
+            seek(0, kt0);
+        const int n = kt1 - kt0;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (s < n)
+                issue(s);
+        wait_younger<S - 1, LPT>(min(S - 1, n - 1));
+        read(I0{}, 0);
+        int slot = 0;
+        auto stage = [&](auto SET, auto OTHER, int k) __attribute__((always_inline)) {
+            constexpr int set = decltype(SET)::value;
+            const int next = slot + 1 == S ? 0 : slot + 1;
+            if (k + 1 < n) {
+                wait_younger<S - 2, LPT>(min(S - 2, n - 2 - k));
+                if (k + S < n)
+                    issue(slot);
+                read(OTHER, next);
+            }
+            slot = next;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < SP::NB; ++j)
+#pragma unroll
+                        for (int i = 0; i < SQ::NB; ++i)
+                            acc[h][j][q][i] =
+                                ffn_mfma<FP8>(fp[set][h][j], fq[set][q][i], acc[h][j][q][i]);
+        };
+        for (int k = 0; k < n; k += 2) {
+            stage(I0{}, I1{}, k);
+            if (k + 1 < n)
+                stage(I1{}, I0{}, k + 1);
+        }
     }
     ffn_finish<SP, SQ, DUAL, EPI>(a, acc, c0, r0, tile_r, wp, wq, WQ, lane);
 }
