@@ -63,7 +63,7 @@ void set_forward(FfnArgs& a, const void* A, const void* B0, const void* B1, int6
 
 int forward_splits(int64_t M, int64_t N, int64_t K, int64_t esz)
 {
-    return M <= kFfnSkinnyRows ? 1 : ffn_splits(M, N, stages(K, esz));
+    return ffn_skinny_fits(EPI_LINEAR, M, N, K * esz) ? 1 : ffn_splits(M, N, stages(K, esz));
 }
 
 int run_linear(int fp8, const void* A, const void* B, const float* sa, const float* sb,
@@ -92,7 +92,7 @@ int run_linear(int fp8, const void* A, const void* B, const float* sa, const flo
     a.sp[0] = sb;
     a.bias = (const uint16_t*)bias;
     a.res = (const uint16_t*)residual;
-    if (M <= kFfnSkinnyRows)
+    if (ffn_skinny_fits(EPI_LINEAR, M, N, K * esz))
         return hip_status(ffn_launch_skinny(fp8, EPI_LINEAR, a, (hipStream_t)stream));
     a.splits = forward_splits(M, N, K, esz);
     if (a.splits > 1) {
@@ -130,7 +130,7 @@ int run_gated(int fp8, const void* A, const void* Bg, const void* Bu, const floa
     a.sq = sa;
     a.sp[0] = sg;
     a.sp[1] = su;
-    if (M <= kFfnSkinnyRows)
+    if (ffn_skinny_fits(EPI_GATED, M, N, K * esz))
         return hip_status(ffn_launch_skinny(fp8, EPI_GATED, a, (hipStream_t)stream));
     return hip_status(ffn_launch(fp8, LAY_NT, EPI_GATED, a, (hipStream_t)stream));
 }

@@ -75,9 +75,10 @@ bool ffn_pair_fits(const FfnArgs& in, const FfnArgs& w);
 hipError_t ffn_launch_pair(const FfnArgs& in, const FfnArgs& w, hipStream_t stream);
 // Sum of the Split-K pieces followed by EPI_LINEAR.
 hipError_t ffn_launch_reduce(const FfnArgs& a, hipStream_t stream);
-// Few rows (R <= kFfnSkinnyRows): one pass over the weights, K split over the
-// waves of a workgroup.  EPI_LINEAR or EPI_GATED, both operands K-contiguous.
-constexpr int kFfnSkinnyRows = 16;
+// Few rows: one pass over the weights, K split over the waves of a workgroup.
+// EPI_LINEAR or EPI_GATED, both operands K-contiguous; R <= 32, and
+// ffn_skinny_fits says where it is the faster way (always up to 16 rows).
+bool ffn_skinny_fits(int epi, int64_t R, int64_t C, int64_t kbytes);
 hipError_t ffn_launch_skinny(int fp8, int epi, const FfnArgs& a, hipStream_t stream);
 
 // Column sums of bf16 x [R][C] over strips of kColsumRows rows -> fp32

@@ -1,4 +1,4 @@
-// Feed-forward products for few rows (R <= 16, decoding): out = epilogue of
+// Feed-forward products for few rows (R <= 32, decoding): out = epilogue of
 // Q [R][K] times the weights P [C][K], bound by reading the weights once.
 //
 // A workgroup owns COLS output columns and its W waves split K: step s of 128
@@ -6,27 +6,27 @@
 // of each of its weight rows at a time.  Operands go from global memory to
 // registers in the matrix cores' layout (the weights on the row side, the
 // tokens on the column side).  The W partial sums are added through LDS in
-// wave order.  Measured and not kept (M = 1 to 16, N = 2048 to 12288): two or
-// four steps in flight per wave, 4 or 16 waves, two or four blocks of columns
+// wave order.  Past 16 rows a second block of tokens (TB = 2) meets the same
+// weight registers.  Measured and not kept (M = 1 to 16, N = 2048 to 12288): two
+// or four steps in flight per wave, 4 or 16 waves, two or four blocks of columns
 // per workgroup; each wins a few percent on some size and loses as much or
 // more on others (N = 2048, K = 6144, M = 4, bf16: 8.9 us, the others 8.8 to
 // 21; gated N = 12288, K = 4096, M = 1: 38.8 us = 5.2 TB/s, the others 35.8 to
-// 62).  The gated form puts 8
-// gate rows and 8 up rows in one 16-row block; the linear form 16 rows, or 8
-// (the other half of the block stays zero) where 16 would leave compute units
-// without a workgroup.
+// 62).  The gated form puts 8 gate rows and 8 up rows in one 16-row block; the
+// linear form 16 rows, or 8 (the other half of the block stays zero) where 16
+// would leave compute units without a workgroup.
 #pragma once
 
 #include "ffn_epilogue.h"
 
 namespace qll {
 
-template <bool FP8, int EPI, int COLS, int W>
+template <bool FP8, int EPI, int COLS, int TB, int W>
 __global__ __launch_bounds__(W * 64) void ffn_skinny_kernel(FfnArgs a)
 {
     constexpr bool DUAL = EPI == EPI_GATED;
     static_assert(DUAL ? COLS == 8 : (COLS == 8 || COLS == 16), "columns of a block");
-    static_assert(W >= 4, "a thread per sum");
+    static_assert(W >= 4 * TB, "a thread per sum");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
@@ -45,12 +45,17 @@ __global__ __launch_bounds__(W * 64) void ffn_skinny_kernel(FfnArgs a)
     const int row = COLS == 8 ? (i & 7) : i;
     const uint8_t* pp = (i >= 8 ? a.P[1] : a.P[0]) + (size_t)min(c0 + row, a.C - 1) * a.ldp + g * 16;
     const uint32_t vp = i < COLS ? (uint32_t)row * (uint32_t)a.ldp + g * 16 : kOutOfRange;
-    const uint32_t vq = i < a.R ? (uint32_t)i * (uint32_t)a.ldq + g * 16 : kOutOfRange;
-
-    v4f acc = {0, 0, 0, 0};
+    uint32_t vq[TB];
+    v4f acc[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        const int r = 16 * t + i;
+        vq[t] = r < a.R ? (uint32_t)r * (uint32_t)a.ldq + g * 16 : kOutOfRange;
+        acc[t] = v4f{0, 0, 0, 0};
+    }
     const int steps = (kbytes + 127) >> 7;
     for (int s = wave; s < steps; s += W) {
-        uint4 p[2], q[2];
+        uint4 p[2], q[TB][2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             const int off = s * 128 + ks * 64;
@@ -63,22 +68,31 @@ __global__ __launch_bounds__(W * 64) void ffn_skinny_kernel(FfnArgs a)
                 p[ks] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                                       rp, (int)(in ? vp + off : kOutOfRange), 0, 0));
             }
-            q[ks] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rq, (int)(in ? vq + off : kOutOfRange), 0, 0));
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                q[t][ks] = __builtin_bit_cast(
+                    uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                               rq, (int)(in ? vq[t] + off : kOutOfRange), 0, 0));
         }
-        if constexpr (FP8) {
-            acc = mfma_step<OP_FP8>(p, q, acc);
-        } else {
-            acc = mfma_step<OP_BF16>(&p[0], &q[0], acc);
-            acc = mfma_step<OP_BF16>(&p[1], &q[1], acc);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            if constexpr (FP8) {
+                acc[t] = mfma_step<OP_FP8>(p, q[t], acc[t]);
+            } else {
+                acc[t] = mfma_step<OP_BF16>(&p[0], &q[t][0], acc[t]);
+                acc[t] = mfma_step<OP_BF16>(&p[1], &q[t][1], acc[t]);
+            }
         }
     }
 
     // partial sums [wave][token][block row]
-    __shared__ __attribute__((aligned(16))) float red[W][16][16];
-    *(float4*)&red[wave][i][g * 4] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __shared__ __attribute__((aligned(16))) float red[W][TB * 16][16];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+        *(float4*)&red[wave][16 * t + i][g * 4] =
+            make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    if (threadIdx.x < 256) {
+    if (threadIdx.x < TB * 256) {
         const int br = threadIdx.x & 15, r = threadIdx.x >> 4;
         float v = 0.0f;
 #pragma unroll

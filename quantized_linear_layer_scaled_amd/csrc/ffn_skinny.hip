@@ -12,12 +12,12 @@ hipError_t ffn_launch_nn(int, int, const FfnArgs&, hipStream_t);
 hipError_t ffn_launch_tn(int, int, const FfnArgs&, hipStream_t);
 
 // Measured per call (us): the 256x256 tile against the 128x128 ones, gated FP8
-// M = 1024, N = 6144, K = 2048 (192 tiles of the 256 CUs): 28 / 36; FP8
-// M = 2048, N = 4096, K = 12288 (128 tiles): 121 / 97.  128x128 over 4 waves,
+// M = 1024, N = 6144, K = 2048 (192 tiles of the 256 CUs): 28.8 / 36.1; FP8
+// M = 2048, N = 4096, K = 12288 (128 tiles): 105 / 90.  128x128 over 4 waves,
 // two workgroups per CU, against 8 waves and a deeper ring: bf16 M = 1024,
-// N = K = 4096 (256 tiles) 55.7 / 46.8; gated bf16 M = 300, N = 6144, K = 2048
-// (288 tiles) 30.2 / 48.5.  128x128 against 64x64: M = 512, N = 4096, K = 2048
-// (128 tiles) 26.1 / 23.3.
+// N = K = 4096 (256 tiles) 49.7 / 44.5; gated bf16 M = 300, N = 6144, K = 2048
+// (288 tiles) 29.3 / 42.1.  128x128 against 64x64: M = 512, N = 4096, K = 2048
+// (128 tiles) 25.7 / 20.5; FP8 M = 1024, N = K = 4096 (256 tiles) 25.8 / 34.3.
 int ffn_tile_pick(int64_t R, int64_t C, int epi)
 {
     if (ffn_tiles(0, R, C, epi) >= 176)
@@ -32,16 +32,21 @@ int ffn_dz_strips(int64_t R, int64_t C)
     return (int)((R + t.rows - 1) / t.rows) * t.wave_rows;
 }
 
-// Split-K: about three workgroups per CU, of at least 16 stages each (input
-// gradient M = 512, N = 6144, K = 2048: 43 us unsplit, 36 with two pieces, 37
-// with four; M = 256, N = 2048, K = 6144: 44, 28, 23).
+// Split-K: at most one workgroup per CU and at least 12 stages each.  Unsplit,
+// this many pieces (in brackets) and more (us): bf16 M = 64, N = 4096,
+// K = 12288 65.6, 26.2 (4), 28.9 with eight; FP8 the same 33.1, 16.8 (4), 19.3;
+// bf16 M = 128, N = 4096, K = 2048 14.6, 13.7 (2), 15.1 with four.  Where the
+// tiles are as many as the CUs, pieces write more than they gain: FP8 M = 512,
+// N = 2048, K = 6144 19.9, 23.1 with three; bf16 M = 512, N = K = 2048 15.2,
+// 18.0 with two (long bf16 products gain there: M = 512, N = 2048, K = 6144
+// 33.9, 29.0 with two; FP8 M = 256, N = 4096, K = 12288 loses, 34.8, 37.4).
 int ffn_splits(int64_t R, int64_t C, int64_t stages)
 {
     const int64_t tiles = ffn_tiles(kFfnSmallest, R, C, EPI_LINEAR);
     if (tiles == 0 || ffn_tile_pick(R, C, EPI_LINEAR) != kFfnSmallest)
         return 1;
-    const int64_t by_tiles = 768 / tiles;
-    const int64_t s = by_tiles < stages / 16 ? by_tiles : stages / 16;
+    const int64_t by_tiles = 256 / tiles;
+    const int64_t s = by_tiles < stages / 12 ? by_tiles : stages / 12;
     return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
 }
 
@@ -67,13 +72,34 @@ hipError_t ffn_launch(int fp8, int layout, int epi, FfnArgs a, hipStream_t strea
     return ffn_launch_reduce(a, stream);
 }
 
+// From 17 rows on a workgroup here re-reads the tokens for every 8 or 16
+// columns, and the 64x64 tile for every 64 (gated 32), so the tile wins once the
+// weights are many.  Measured, this kernel / the tile (us) at 17 and 32 rows:
+// linear FP8 N = 4096, K = 2048 (8 MB) 5.4 / 9.0, 6.0 / 8.9; bf16 the same (17
+// MB) 8.1 / 11.6, 8.7 / 11.7; FP8 N = 2048, K = 6144 (13 MB) 8.2 / 11.6, 10.1 /
+// 12.0; bf16 the same (25 MB) 14.1 / 12.4, 17.1 / 13.4; FP8 N = 4096, K = 12288
+// (50 MB) 15.3 / 15.4, 19.2 / 15.4; bf16 N = 12288, K = 4096 28.0 / 23.7, 35.1 /
+// 23.9.  The gated tile does not split K, so its time goes with K alone until
+// its tiles fill the chip, and the columns decide: bf16 N = 2048, K = 6144 15.3
+// / 34.0, 19.0 / 34.1; N = 4096, K = 2048 11.2 / 13.7, 14.1 / 14.0; N = 12288,
+// K = 4096 50.2 / 38.8, 66.0 / 38.6.
+bool ffn_skinny_fits(int epi, int64_t R, int64_t C, int64_t kbytes)
+{
+    if (R <= 16 || R > 32)
+        return R <= 16;
+    return epi == EPI_GATED ? C <= 4096 : C * kbytes <= (int64_t{1} << 24);
+}
+
 namespace {
 
 template <bool FP8, int EPI, int COLS>
 hipError_t skinny(const FfnArgs& a, hipStream_t stream)
 {
-    ffn_skinny_kernel<FP8, EPI, COLS, 8>
-        <<<(unsigned)((a.C + COLS - 1) / COLS), 512, 0, stream>>>(a);
+    const unsigned grid = (unsigned)((a.C + COLS - 1) / COLS);
+    if (a.R <= 16)
+        ffn_skinny_kernel<FP8, EPI, COLS, 1, 8><<<grid, 512, 0, stream>>>(a);
+    else
+        ffn_skinny_kernel<FP8, EPI, COLS, 2, 8><<<grid, 512, 0, stream>>>(a);
     return hipGetLastError();
 }
 

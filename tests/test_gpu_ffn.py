@@ -54,7 +54,9 @@ def check(y, want, what, whole=None):
 
 # M: one token, decode blocks, the first tile sizes, ragged tiles; N: one
 # column, less than a vector, odd, ragged tiles; K: one chunk, ragged stages
-SIZES = [(1, 64, 128), (1, 1, 16), (3, 9, 48), (16, 129, 272), (17, 40, 1040), (33, 257, 528),
+SIZES = [(1, 64, 128), (1, 1, 16), (3, 9, 48), (16, 129, 272), (17, 40, 1040),
+         # two blocks of tokens: the few-row kernel and, past its rules, the tile
+         (24, 4104, 272), (32, 4099, 144), (31, 2056, 13392), (32, 8200, 80), (33, 257, 528),
          (64, 520, 1056), (65, 64, 128), (65, 7, 32), (100, 333, 1040), (129, 130, 64), (200, 1000, 4112),
          (257, 264, 656), (300, 2056, 400), (1025, 1041, 144),
          # the 256x256 tile: one, two and several stages, ragged
