@@ -9,7 +9,8 @@
 namespace qll {
 namespace {
 
-constexpr int64_t kMaxDim = 0x3FFFFFFF;
+// (64 rows per 256-thread workgroup of a column sum stay below 2^32 threads)
+constexpr int64_t kMaxDim = 0x3FFFFF00;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 // a tile addresses up to 256 rows of an operand with 31-bit byte offsets
 constexpr int64_t kMaxRowBytes = (((int64_t)1 << 31) - 1) / 256;

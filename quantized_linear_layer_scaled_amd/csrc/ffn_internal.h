@@ -77,7 +77,7 @@ hipError_t ffn_launch_pair(const FfnArgs& in, const FfnArgs& w, hipStream_t stre
 hipError_t ffn_launch_reduce(const FfnArgs& a, hipStream_t stream);
 // Few rows: one pass over the weights, K split over the waves of a workgroup.
 // EPI_LINEAR or EPI_GATED, both operands K-contiguous; R <= 32, and
-// ffn_skinny_fits says where it is the faster way (always up to 16 rows).
+// ffn_skinny_fits says where it is the way to go.
 bool ffn_skinny_fits(int epi, int64_t R, int64_t C, int64_t kbytes);
 hipError_t ffn_launch_skinny(int fp8, int epi, const FfnArgs& a, hipStream_t stream);
 

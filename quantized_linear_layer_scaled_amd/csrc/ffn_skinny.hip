@@ -82,9 +82,12 @@ hipError_t ffn_launch(int fp8, int layout, int epi, FfnArgs a, hipStream_t strea
 // 23.9.  The gated tile does not split K, so its time goes with K alone until
 // its tiles fill the chip, and the columns decide: bf16 N = 2048, K = 6144 15.3
 // / 34.0, 19.0 / 34.1; N = 4096, K = 2048 11.2 / 13.7, 14.1 / 14.0; N = 12288,
-// K = 4096 50.2 / 38.8, 66.0 / 38.6.
+// K = 4096 50.2 / 38.8, 66.0 / 38.6.  (Past 2^25 columns 512 threads for each 8
+// or 16 of them would be more than a launch holds; the tiles are walked over.)
 bool ffn_skinny_fits(int epi, int64_t R, int64_t C, int64_t kbytes)
 {
+    if (C > (int64_t{1} << 25))
+        return false;
     if (R <= 16 || R > 32)
         return R <= 16;
     return epi == EPI_GATED ? C <= 4096 : C * kbytes <= (int64_t{1} << 24);

@@ -489,13 +489,16 @@ __global__ __launch_bounds__(256) void residual_norm_vectors_kernel(NormArgs a)
 
 namespace {
 
+// a launch holds less than 2^32 threads
+constexpr int kMostRows = 1 << 21;
+
 template <int T, int CH>
 hipError_t forward(const NormArgs& a, hipStream_t s)
 {
     // as many workgroups as the compute units hold threads for; rows of
     // several runs per thread gain nothing from a loop
-    constexpr int most = 256 * (2048 / T);
-    const unsigned grid = (unsigned)(a.M < most || CH > 1 ? a.M : most);
+    constexpr int most = CH > 1 ? kMostRows : 256 * (2048 / T);
+    const unsigned grid = (unsigned)(a.M < most ? a.M : most);
     auto go = [&](auto HY, auto F, auto Q) {
         residual_norm_kernel<T, CH, decltype(HY)::value, decltype(F)::value, decltype(Q)::value>
             <<<grid, T, 0, s>>>(a);
@@ -519,7 +522,7 @@ template <int T, int CH, bool SUMS>
 hipError_t backward(const NormArgs& a, hipStream_t s)
 {
     const unsigned blocks = (unsigned)norm_backward_blocks(a.M, a.K);
-    const unsigned grid = SUMS ? blocks : (unsigned)a.M;
+    const unsigned grid = SUMS ? blocks : (unsigned)(a.M < kMostRows ? a.M : kMostRows);
     const dim3 strips(blocks, (unsigned)((a.K / 8 + 255) / 256));
     auto go = [&](auto HY, auto F) {
         residual_norm_backward_kernel<T, CH, decltype(HY)::value, decltype(F)::value, SUMS>

@@ -265,6 +265,50 @@ NORM_SIZES = [(1, 16), (1, 4096), (3, 512), (2, 528), (7, 2048), (5, 2064), (3, 
               (4, 8208), (2, 16384), (3, 32768), (1030, 1040), (1030, 4096), (1025, 6160)]
 
 
+def test_more_columns_than_one_launch_of_few_row_workgroups(qll):
+    """One token and so many columns that 512 threads for each 8 of them would
+    be 2^32 threads."""
+    g = gen(81)
+    N, K = (1 << 26) + 72, 16
+    codes = [torch.randint(0, 120, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+             .view(torch.float8_e4m3fn) for _ in range(2)]
+    x = torch.randint(0, 120, (1, K), generator=g, device="cuda",
+                      dtype=torch.uint8).view(torch.float8_e4m3fn)
+    sa = torch.full((1,), 1e-3, device="cuda")
+    sb = torch.rand(N, generator=g, device="cuda") * 1e-3
+    cols = torch.cat([torch.arange(64, device="cuda"), torch.arange(N - 200, N, device="cuda"),
+                      torch.randint(0, N, (2000,), generator=g, device="cuda")])
+    w = [c.view(torch.uint8)[cols].view(torch.float8_e4m3fn).to(D) for c in codes]
+    y = qll.gemm_fp8_epilogue(x, codes[0], sa, sb)
+    check(y[:, cols], ref.linear(x.to(D), w[0], sa.to(D), sb[cols].to(D)), "linear")
+    y = qll.gated_fp8(x, codes[0], codes[1], sa, sb, sb)
+    check(y[:, cols], ref.gated(x.to(D), w[0], w[1], sa.to(D), sb[cols].to(D),
+                                sb[cols].to(D)), "gated")
+
+
+@pytest.mark.parametrize("K,backward", [(4104, False), (8200, True)])
+def test_more_long_rows_than_workgroups(qll, K, backward):
+    """More rows than a launch of one workgroup per row may hold: each row's
+    results are those of a call on few rows, bit for bit."""
+    g = gen(82)
+    M, P = (1 << 21) + 1100, 1031
+    base, w = rnd(g, P, K), rnd(g, K)
+    x = torch.empty((M, K), dtype=BF, device="cuda")
+    for i in range(0, M, P):
+        x[i:i + P] = base[:min(P, M - i)]
+    if backward:
+        want = qll.residual_norm_backward(None, base, w, base)[1]
+        got = qll.residual_norm_backward(None, x, w, x)[1]
+    else:
+        want, got = qll.residual_norm(None, base, w)[1], qll.residual_norm(None, x, w)[1]
+    bad = torch.zeros((), dtype=torch.bool, device="cuda")
+    for i in range(0, M, P):
+        bad |= (got[i:i + P] != want[:min(P, M - i)]).any()
+    assert not bool(bad)
+    del x, got
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("M,K", NORM_SIZES)
 @pytest.mark.parametrize("stream", ["bf16", "fp32"])
 def test_residual_norm(qll, stream, M, K):
