@@ -28,15 +28,23 @@ namespace qll {
 
 namespace {
 
-// Sum (or maximum) over the T threads of a row, in every thread.  `red`: one
-// float per wave, not reused before the next barrier of the caller's rows.
+// The larger of two magnitudes, a NaN if either is one: the order of their
+// bits, in which a NaN is above infinity (fmaxf drops it).
+__device__ __forceinline__ float magnitude_max(float a, float b)
+{
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// Sum (or maximum, of magnitudes) over the T threads of a row, in every
+// thread.  `red`: one float per wave, not reused before the next barrier of
+// the caller's rows.
 template <int T, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* red)
 {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const float o = __shfl_xor(v, d, 64);
-        v = MAX ? fmaxf(v, o) : v + o;
+        v = MAX ? magnitude_max(v, o) : v + o;
     }
     if constexpr (T > 64) {
         constexpr int WV = T / 64;
@@ -47,7 +55,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red)
         v = red[0];
 #pragma unroll
         for (int w = 1; w < WV; ++w)
-            v = MAX ? fmaxf(v, red[w]) : v + red[w];
+            v = MAX ? magnitude_max(v, red[w]) : v + red[w];
     }
     return v;
 }
@@ -210,7 +218,7 @@ __global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[j][e] = h[j][e] * ih * w2[e];
-                amax = fmaxf(amax, fabsf(h[j][e]));
+                amax = magnitude_max(amax, fabsf(h[j][e]));
             }
             if constexpr (!QUANT) {
                 if (c < K)
@@ -218,7 +226,10 @@ __global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a)
             }
         }
         if constexpr (QUANT) {
-            // the rule of quantize_per_token_fp8, on the fp32 values
+            // The rule of quantize_per_token_fp8, on the fp32 values.  A row
+            // whose maximum is a NaN or infinite has that scale and takes the
+            // division, whose NaN the clamp below keeps (clamp448 does not):
+            // no codes make such a row look like a finite one.
             amax = row_reduce<T, true>(amax, red[par][2]);
             const Quot q(amax / 448.0f);
             if (t == 0)
@@ -233,8 +244,10 @@ __global__ __launch_bounds__(T) void residual_norm_kernel(NormArgs a)
                         f[e] = clamp448(q.by_reciprocal(h[j][e]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = q.s == 0.0f ? 0.0f : clamp448(h[j][e] / q.s);
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = q.s == 0.0f ? 0.0f : h[j][e] / q.s;
+                        f[e] = v > 448.0f ? 448.0f : (v < -448.0f ? -448.0f : v);
+                    }
                 }
                 int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
                 w0 = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w0, true);

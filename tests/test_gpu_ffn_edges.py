@@ -1,0 +1,66 @@
+"""GPU tests of the feed-forward operators at their edges: empty batches, rows
+that are not finite, activations far from zero, and the paths that only some
+sizes take.  Formulas and bounds: tests/ffn_reference.py."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import ffn_reference as ref  # noqa: E402
+from test_gpu_ffn import BF, D, F32, check, gen, guarded, qll, rnd  # noqa: E402,F401
+
+NAN, INF = float("nan"), float("inf")
+
+
+# --------------------------------------------------------------------------
+# rows that are not finite
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K", [(3, 16), (5, 4096), (4, 6160), (1100, 2048), (3, 32768)])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_bad_rows_of_the_e4m3_norm(qll, stream, post, M, K):
+    """A row with a NaN or an infinity has a NaN scale (its normed values are
+    NaN where the row's rms or the value is), never a clean zero row; NaN
+    normed values have NaN codes; the other rows keep their bits."""
+    g = gen(M + K)
+    st = BF if stream == "bf16" else F32
+    y, r = rnd(g, M, K), rnd(g, M, K, dtype=st)
+    w, w1 = rnd(g, K, std=0.2) + 1, (rnd(g, K, std=0.2) + 1 if post else None)
+    at = M // 2
+    rest = [m for m in range(M) if m != at]
+    _, q0, s0 = qll.residual_norm(y, r, w, w_post=w1, quantize=True)
+    for block in (True, False):
+        clean = (s0, q0) if block else qll.residual_norm(None, r, w, quantize=True)[:0:-1]
+        for which in ("y", "r"):
+            for bad in (NAN, INF, -INF):
+                if which == "y" and not block:
+                    continue
+                y2, r2 = y.clone(), r.clone()
+                (y2 if which == "y" else r2)[at, K - 1] = bad
+                a = (y2 if block else None, r2, w)
+                kw = dict(w_post=w1 if block else None)
+                n = qll.residual_norm(*a, **kw)[1].float()
+                _, q, s = qll.residual_norm(*a, quantize=True, **kw)
+                what = (which, bad, block)
+                assert torch.isnan(n[at]).any(), what
+                assert torch.isnan(s[at]).all(), what
+                assert torch.isnan(q[at].float()).all(), what
+                assert torch.equal(s[rest], clean[0][rest]), what
+                assert torch.equal(q.view(torch.uint8)[rest], clean[1].view(torch.uint8)[rest]), what
+
+
+def test_infinite_normed_values_of_the_e4m3_norm(qll):
+    """An infinite norm weight: an infinite scale, by the formula, under which
+    infinite values have NaN codes and finite ones zero codes."""
+    g = gen(3)
+    r, w = rnd(g, 4, 64) + 3, rnd(g, 64, std=0.2) + 1
+    w[7] = INF
+    _, q, s = qll.residual_norm(None, r, w, quantize=True)
+    q = q.float()
+    assert torch.isinf(s).all() and torch.isnan(q[:, 7]).all()
+    assert (torch.cat([q[:, :7], q[:, 8:]], 1) == 0).all()
+
+
