@@ -286,8 +286,9 @@ int gemm_bf16_epilogue_backward(const void* A, const void* B, const void* dout, 
     int rc = validate_backward(M, N, K, act);
     if (rc != QLL_OK)
         return rc;
+    // (without rows dA is empty, and an empty tensor's address may be NULL)
     if (!dB && !dbias && (!dA || M == 0))
-        return dA ? QLL_OK : QLL_ERR_INVALID_ARG;
+        return M == 0 ? QLL_OK : QLL_ERR_INVALID_ARG;
     if (!B || (M > 0 && (!A || !dout)))
         return QLL_ERR_INVALID_ARG;
     if (misaligned(A, 16) || misaligned(B, 16) || misaligned(dout, 16) || misaligned(bias, 16) ||
@@ -359,7 +360,7 @@ int gated_bf16_backward(const void* A, const void* Bg, const void* Bu, const voi
     if ((dBg == nullptr) != (dBu == nullptr))
         return QLL_ERR_INVALID_ARG;
     if (!dBg && (!dA || M == 0))
-        return dA ? QLL_OK : QLL_ERR_INVALID_ARG;
+        return M == 0 ? QLL_OK : QLL_ERR_INVALID_ARG;
     if (!Bg || !Bu || (M > 0 && (!A || !dout)))
         return QLL_ERR_INVALID_ARG;
     if (misaligned(A, 16) || misaligned(Bg, 16) || misaligned(Bu, 16) || misaligned(dout, 16) ||

@@ -15,6 +15,25 @@ NAN, INF = float("nan"), float("inf")
 
 
 # --------------------------------------------------------------------------
+# empty batches
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_no_tokens_with_frozen_weights(qll, act):
+    """No tokens and the input's gradient alone (an empty tensor's address is
+    null): an empty gradient, as for the forward calls."""
+    g = gen(1)
+    x, d = torch.empty(0, 64, dtype=BF, device="cuda"), torch.empty(0, 24, dtype=BF, device="cuda")
+    w, b = rnd(g, 24, 64), rnd(g, 24)
+    dA, dB, db = qll.gemm_bf16_epilogue_backward(x, w, d, act=act, need_weight=False)
+    assert dA.shape == (0, 64) and dB is None and db is None
+    dA, dB, db = qll.gemm_bf16_epilogue_backward(x, w, d, bias=b, act=act, need_weight=False)
+    assert dA.shape == (0, 64) and dB is None and (db == 0).all()
+    got = qll.gated_bf16_backward(x, w, w, d, need_weight=False)
+    assert got[0].shape == (0, 64) and got[1] is None and got[2] is None
+
+
+# --------------------------------------------------------------------------
 # rows that are not finite
 # --------------------------------------------------------------------------
 
