@@ -74,7 +74,8 @@ __device__ __forceinline__ void act_slope(float z, float& f, float& d)
         d = cdf + z * (kInvSqrt2Pi * e);
     } else if constexpr (ACT == ACT_GELU_TANH) {
         // past +-16 the sigmoid is 0 or 1 in fp32, and z^3 cannot overflow
-        const float zc = fminf(fmaxf(z, -16.0f), 16.0f);
+        // (comparisons, which keep a NaN; fminf and fmaxf drop it)
+        const float zc = z > 16.0f ? 16.0f : (z < -16.0f ? -16.0f : z);
         const float q = sigmoid_f(2.0f * kGeluA * (zc + kGeluB * zc * zc * zc));
         f = z * q;
         d = q + zc * q * (1.0f - q) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * zc * zc);

@@ -83,3 +83,30 @@ def test_infinite_normed_values_of_the_e4m3_norm(qll):
     assert (torch.cat([q[:, :7], q[:, 8:]], 1) == 0).all()
 
 
+@pytest.mark.parametrize("M", [5, 70, 300])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "sigmoid"])
+def test_a_bad_token_has_bad_gradients(qll, act, M):
+    """A NaN pre-activation has a NaN slope: the token's own gradient, and
+    those of the weights and biases, which sum over the tokens, show it."""
+    N, K = 200, 80
+    g = gen(M)
+    x, wg, wu, dout, b = rnd(g, M, K), rnd(g, N, K), rnd(g, N, K), rnd(g, M, N), rnd(g, N)
+    x[M // 2] = NAN
+    rest = [m for m in range(M) if m != M // 2]
+    for bias in (b, None):
+        dA, dB, db = qll.gemm_bf16_epilogue_backward(x, wg, dout, bias=bias, act=act)
+        assert torch.isnan(dA[M // 2]).all() and torch.isfinite(dA[rest]).all()
+        assert torch.isnan(dB).all() and (bias is None or torch.isnan(db).all())
+    # the gate's pre-activation alone: through its weights
+    clean = x.clone()
+    clean[M // 2] = 1
+    bad = wg.clone()
+    bad[3] = NAN
+    dA, dB, db = qll.gemm_bf16_epilogue_backward(clean, bad, dout, bias=b, act=act, need_input=False)
+    assert torch.isnan(dB[3]).all() and torch.isnan(db[3])
+    assert torch.isfinite(dB[:3]).all() and torch.isfinite(dB[4:]).all() and torch.isfinite(db[:3]).all()
+    _, dBg, dBu = qll.gated_bf16_backward(clean, bad, wu, dout, act=act, need_input=False)
+    for t in (dBg, dBu):
+        assert torch.isnan(t[3]).all() and torch.isfinite(t[:3]).all() and torch.isfinite(t[4:]).all()
+
+
