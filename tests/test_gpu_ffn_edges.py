@@ -110,3 +110,33 @@ def test_a_bad_token_has_bad_gradients(qll, act, M):
         assert torch.isnan(t[3]).all() and torch.isfinite(t[:3]).all() and torch.isfinite(t[4:]).all()
 
 
+# --------------------------------------------------------------------------
+# activations far from zero: bounds relative to the value itself
+# --------------------------------------------------------------------------
+
+def diagonal(z):
+    """x [M][K], w [N][K] with x w^T = z in every row, exactly: one product of
+    z[n] with 1, the rest zero."""
+    N = z.numel()
+    return torch.ones(70, N, dtype=BF, device="cuda"), torch.diag(z).to(BF).contiguous()
+
+
+@pytest.mark.parametrize("M", [1, 70])
+def test_gelu_is_accurate_relative_to_itself(qll, M):
+    """gelu(z) = z Phi(z) in fp32, the product exact.  Phi(z) is e^(-z^2/2)
+    times a function fitted to 2^-23; the exponent is off by z^2/2 times 2.5
+    u (its square, its product, the constant), u = 2^-24; the exponential and
+    the reciprocal by 2 u each, ten roundings of at most u follow: at most
+    (1.25 z^2 + 16) u of the result.  The exponential keeps its bits down to
+    2^-126, z = -13."""
+    z = torch.cat([torch.linspace(-12, 12, 769), torch.linspace(-3, 3, 511)]).to(BF)
+    z = torch.cat([z, z[:1280 - z.numel()]]).cuda()
+    x, w = diagonal(z)
+    got = qll.gemm_bf16_epilogue(x[:M], w, act="gelu", out_dtype="fp32").to(D)
+    zd = z.to(D)
+    want = zd * 0.5 * torch.special.erfc(-zd / math.sqrt(2))
+    bound = (1.25 * zd * zd + 16) * 2.0 ** -24 * want.abs()
+    for m in range(M):
+        check(got[m], (want, bound), ("gelu", m))
+
+
