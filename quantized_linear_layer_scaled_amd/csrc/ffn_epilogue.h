@@ -10,8 +10,9 @@ namespace qll {
 
 __device__ __forceinline__ float bf16_value(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
-// 1 / (1 + e^-z); the reciprocal and the exponential are the hardware's
-// (about 1 ulp each), far below the rounding of a bf16 result.
+// 1 / (1 + e^-z); the reciprocal and the exponential of two are the hardware's
+// (about 1 ulp each), and the exponent's rounding moves e^-z by |z| 2^-24 of
+// itself: far below the rounding of a bf16 result.
 __device__ __forceinline__ float sigmoid_f(float z)
 {
     return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
@@ -91,8 +92,11 @@ __device__ __forceinline__ void act_slope(float z, float& f, float& d)
         f = z * q;
         d = q * (1.0f + z * (1.0f - q));
     } else if constexpr (ACT == ACT_SIGMOID) {
-        f = sigmoid_f(z);
-        d = f * (1.0f - f);
+        // f (1 - f) from e^-|z|: 1 - f would cancel where f is next to 1
+        const float e = __expf(-fabsf(z));
+        const float r = __builtin_amdgcn_rcpf(1.0f + e);
+        f = z < 0.0f ? e * r : r;
+        d = e * r * r;
     } else {
         f = z;
         d = 1.0f;

@@ -140,3 +140,19 @@ def test_gelu_is_accurate_relative_to_itself(qll, M):
         check(got[m], (want, bound), ("gelu", m))
 
 
+def test_sigmoid_slope_is_accurate_relative_to_itself(qll):
+    """dA[m][k] = sigma'(z_k) z_k: two roundings to bf16 (dz and dA; the weight is
+    exact) and fp32 arithmetic, on both sides of zero."""
+    z = torch.cat([torch.linspace(-24, 24, 97), torch.linspace(-3, 3, 31)]).to(BF).cuda()
+    x, w = diagonal(z)
+    zd = z.to(D)
+    want = torch.sigmoid(zd) * torch.sigmoid(-zd) * zd
+    dA, _, db = qll.gemm_bf16_epilogue_backward(x, w, torch.ones(70, z.numel(), dtype=BF, device="cuda"),
+                                                bias=torch.zeros_like(z), act="sigmoid")
+    for m in (0, 69):
+        check(dA[m], (want, 2.02 * 2.0 ** -8 * want.abs()), m)
+    want = 70 * torch.sigmoid(zd) * torch.sigmoid(-zd)
+    # each term: the exponent's |z| u, a few roundings; 70 terms summed
+    check(db, (want, (2 * zd.abs() + 16 + 70) * 2.0 ** -24 * want), "dbias")
+
+
