@@ -156,3 +156,95 @@ def test_sigmoid_slope_is_accurate_relative_to_itself(qll):
     check(db, (want, (2 * zd.abs() + 16 + 70) * 2.0 ** -24 * want), "dbias")
 
 
+# --------------------------------------------------------------------------
+# paths that only some sizes take
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K", [(300, 8208), (700, 8200), (300, 16384), (140, 32768)])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_norm_backward_of_many_long_rows(qll, stream, M, K):
+    """Past 8192 columns, with more rows than strips of the vector gradients."""
+    g = gen(M + K)
+    st = BF if stream == "bf16" else F32
+    y, r = rnd(g, M, K), rnd(g, M, K, std=2.0, dtype=st)
+    dn, dr = rnd(g, M, K, std=0.1), rnd(g, M, K, std=0.1, dtype=st)
+    w2, w1, gt = (rnd(g, K, std=0.2) + 1 for _ in range(3))
+    d = lambda t: None if t is None else t.to(D)
+    for post, gate, block, up, al in ((w1, gt, y, dr, 0.75), (None, gt, y, None, 1.0), (None, None, None, dr, 1.0)):
+        want = ref.norm_backward(d(block), d(r), d(w2), d(dn), d(up), d(post), d(gate), al, 0.5)
+        got = qll.residual_norm_backward(block, r, w2, dn, up, w_post=post, gate=gate, alpha=al, beta=0.5)
+        for name, t in zip(("dy", "dr", "dw_pre", "dw_post", "dgate"), got):
+            assert (t is None) == (name not in want), name
+            if t is not None:
+                v, e = want[name]
+                check(t, (v, e + ref.rounding(v, "bf16" if t.dtype == BF else "fp32")), (name, M, K))
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 1160, 264), (64, 1160, 64), (65, 2056, 136), (200, 1544, 72)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_split_input_gradient_across_both_weights(qll, act, M, N, K):
+    """Split-K pieces of the gated input's gradient that cross from the gate's
+    weight to the up projection's, and pieces that start inside the second:
+    pieces of ceil(stages / splits) stages, N / 64 stages per weight."""
+    tiles, seam = -(-M // 64) * -(-K // 64), -(-N // 64)
+    splits = min(256 // tiles, 2 * seam // 12, 32)
+    per = -(-2 * seam // splits)
+    starts = [s * per for s in range(splits)]
+    assert splits > 1 and seam not in starts and any(s > seam for s in starts)
+    g = gen(M + N)
+    x, wg, wu, dout = rnd(g, M, K), rnd(g, N, K, std=0.05), rnd(g, N, K, std=0.05), rnd(g, M, N, std=0.1)
+    want = ref.gated_backward(x.to(D), wg.to(D), wu.to(D), dout.to(D), act)
+    whole, dA = guarded(M, K, BF)
+    got = qll.gated_bf16_backward(x, wg, wu, dout, act=act, dA=dA)
+    for t, r, w, name in zip(got, want, (whole, None, None), ("dA", "dBg", "dBu")):
+        check(t, r, (name, M, N, K), w)
+
+
+# sizes of the 256x256 tile (forward), and of both gradients in one launch
+@pytest.mark.parametrize("M,N,K", [(4100, 4360, 80), (4097, 4105, 208)])
+def test_bad_rows_on_the_large_tile(qll, M, N, K):
+    g = gen(M)
+    x, wg, wu = rnd(g, M, K), rnd(g, N, K), rnd(g, N, K)
+    for m in (0, 300, M - 1):
+        bad = x.clone()
+        bad[m] = NAN
+        rest = torch.arange(M, device="cuda") != m
+        for f in (lambda a: qll.gemm_bf16_epilogue(a, wg, act="silu"), lambda a: qll.gated_bf16(a, wg, wu)):
+            a, b = f(x), f(bad)
+            assert torch.equal(a[rest], b[rest]) and torch.isnan(b[m]).all()
+    for n in (0, 300, N - 1):
+        bad = wg.clone()
+        bad[n] = NAN
+        rest = torch.arange(N, device="cuda") != n
+        for f in (lambda w: qll.gemm_bf16_epilogue(x, w, act="silu"), lambda w: qll.gated_bf16(x, w, wu),
+                  lambda w: qll.gated_bf16(x, wu, w)):
+            a, b = f(wg), f(bad)
+            assert torch.equal(a[:, rest], b[:, rest]) and torch.isnan(b[:, n]).all()
+
+
+# 64x64 tiles, 128x128 tiles, the 256x256 tile in one product, one launch for both
+@pytest.mark.parametrize("M,N,K", [(70, 88, 72), (300, 520, 264), (1600, 1608, 1032), (4100, 4360, 72),
+                                   (2000, 2304, 4360), (4100, 2056, 2056)])
+def test_bad_columns_stay_in_their_gradients(qll, M, N, K):
+    """dA = dz B and dB = dz^T A: a NaN in column k of an operand that is read
+    along its rows changes column k of the gradient and no other, also where
+    a tile reaches past the last column into the next line."""
+    g = gen(M)
+    x, w, dout = rnd(g, M, K), rnd(g, N, K), rnd(g, M, N)
+    dA, dB, _ = qll.gemm_bf16_epilogue_backward(x, w, dout)
+    for k in (0, K // 2, K - 1):
+        rest = torch.arange(K, device="cuda") != k
+        w2, x2 = w.clone(), x.clone()
+        w2[N // 2, k] = NAN
+        x2[M // 3, k] = NAN
+        a, b, _ = qll.gemm_bf16_epilogue_backward(x2, w2, dout)
+        assert torch.equal(a[:, rest], dA[:, rest]) and torch.isnan(a[:, k]).all()
+        assert torch.equal(b[:, rest], dB[:, rest]) and torch.isnan(b[:, k]).all()
+    # (the same launch: either gradient alone may run on another tile)
+    for n in (0, N // 2, N - 1):
+        d2 = dout.clone()
+        d2[M // 2, n] = INF
+        rows, cols = torch.arange(M, device="cuda") != M // 2, torch.arange(N, device="cuda") != n
+        a, b, _ = qll.gemm_bf16_epilogue_backward(x, w, d2)
+        assert torch.equal(a[rows], dA[rows]) and not torch.isfinite(a[M // 2]).any()
+        assert torch.equal(b[cols], dB[cols]) and not torch.isfinite(b[n]).any()
