@@ -52,8 +52,6 @@ void set_forward(FfnArgs& a, const void* A, const void* B0, const void* B1, int6
     a.P[0] = (const uint8_t*)B0;
     a.P[1] = (const uint8_t*)B1;
     a.Q[0] = a.Q[1] = (const uint8_t*)A;
-    a.availP[0] = a.availP[1] = N * K * esz;
-    a.availQ[0] = a.availQ[1] = M * K * esz;
     a.ldp = a.ldq = K * esz;
     a.C = (int)N;
     a.R = (int)M;
@@ -139,7 +137,7 @@ int run_gated(int fp8, const void* A, const void* Bg, const void* Bu, const floa
 // Workspace of a backward pass: the pre-activation gradients, the bias
 // gradient's strips, then Split-K pieces (used by one product at a time).
 struct BackwardPlan {
-    int64_t dz = 0, strips = 0, total = 0;  // byte offsets of the parts, and the end
+    int64_t strips = 0, pieces = 0, total = 0;  // byte offsets behind the first part, and the end
     int64_t nstrips = 0;
     int splits_in = 1, splits_w = 1;
 };
@@ -152,17 +150,14 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int act, bool bias, 
     p.strips = own_dz ? round256(M * width * 2) : 0;
     if (bias)
         p.nstrips = own_dz ? ffn_dz_strips(M, N) : (M + kColsumRows - 1) / kColsumRows;
-    int64_t at = p.strips + round256(p.nstrips * N * 4);
+    p.pieces = p.strips + round256(p.nstrips * N * 4);
     p.splits_in = ffn_splits(M, K, (gated ? 2 : 1) * stages(N, 2));
     p.splits_w = ffn_splits(width, K, stages(M, 2));
     const int64_t in = p.splits_in > 1 ? (int64_t)p.splits_in * M * K * 4 : 0;
     const int64_t w = p.splits_w > 1 ? (int64_t)p.splits_w * width * K * 4 : 0;
-    p.dz = 0;
-    p.total = at + (in > w ? in : w);
+    p.total = p.pieces + (in > w ? in : w);
     return p;
 }
-
-int64_t split_offset(const BackwardPlan& p, int64_t N) { return p.strips + round256(p.nstrips * N * 4); }
 
 // dA [M][K] = dz B, over one (dz, B) or two segments side by side in dz.
 FfnArgs input_gradient(const void* dz, const void* B0, const void* B1, void* dA, int64_t M,
@@ -173,13 +168,10 @@ FfnArgs input_gradient(const void* dz, const void* B0, const void* B1, void* dA,
     a.nseg = nseg;
     a.P[0] = (const uint8_t*)B0;
     a.P[1] = (const uint8_t*)(B1 ? B1 : B0);
-    a.availP[0] = a.availP[1] = N * K * 2;
     a.ldp = K * 2;
     a.ldq = nseg * N * 2;
     a.Q[0] = (const uint8_t*)dz;
     a.Q[1] = a.Q[0] + (nseg - 1) * N * 2;
-    a.availQ[0] = M * a.ldq;
-    a.availQ[1] = a.availQ[0] - (nseg - 1) * N * 2;
     a.C = (int)K;
     a.R = (int)M;
     a.klen = (int)N;
@@ -197,10 +189,8 @@ FfnArgs weight_gradient(const void* dz, const void* A, void* dB0, void* dB1, int
 {
     FfnArgs a = blank();
     a.P[0] = a.P[1] = (const uint8_t*)A;
-    a.availP[0] = a.availP[1] = M * K * 2;
     a.ldp = K * 2;
     a.Q[0] = a.Q[1] = (const uint8_t*)dz;
-    a.availQ[0] = a.availQ[1] = M * width * 2;
     a.ldq = width * 2;
     a.C = (int)K;
     a.R = (int)width;
@@ -304,19 +294,19 @@ int gemm_bf16_epilogue_backward(const void* A, const void* B, const void* dout, 
     hipStream_t s = (hipStream_t)stream;
     uint8_t* w = (uint8_t*)ws;
     float* strips = (float*)(w + p.strips);
-    float* pieces = (float*)(w + split_offset(p, N));
+    float* pieces = (float*)(w + p.pieces);
     const void* dz = dout;
     if (M > 0 && act != ACT_NONE) {
         FfnArgs a = blank();
         set_forward(a, A, B, B, M, N, K, 2);
-        a.out = w + p.dz;
+        a.out = w;
         a.act = act;
         a.bias = (const uint16_t*)bias;
         a.dy = (const uint16_t*)dout;
         a.partial = dbias ? strips : nullptr;
         if (ffn_launch(0, LAY_NT, EPI_DZ, a, s) != hipSuccess)
             return QLL_ERR_HIP;
-        dz = w + p.dz;
+        dz = w;
     } else if (M > 0 && dbias) {
         if (launch_colsum_strips(dout, strips, M, N, s) != hipSuccess)
             return QLL_ERR_HIP;
@@ -375,19 +365,19 @@ int gated_bf16_backward(const void* A, const void* Bg, const void* Bu, const voi
     }
     hipStream_t s = (hipStream_t)stream;
     uint8_t* w = (uint8_t*)ws;
-    float* pieces = (float*)(w + split_offset(p, N));
+    float* pieces = (float*)(w + p.pieces);
     if (M > 0) {
         FfnArgs a = blank();
         set_forward(a, A, Bg, Bu, M, N, K, 2);
-        a.out = w + p.dz;
+        a.out = w;
         a.ldo = 2 * N;
         a.act = act;
         a.dy = (const uint16_t*)dout;
         if (ffn_launch(0, LAY_NT, EPI_DGATED, a, s) != hipSuccess)
             return QLL_ERR_HIP;
     }
-    const FfnArgs in = input_gradient(w + p.dz, Bg, Bu, dA, M, N, K, p.splits_in, pieces);
-    const FfnArgs wt = weight_gradient(w + p.dz, A, dBg, dBu, N, M, 2 * N, K, p.splits_w, pieces);
+    const FfnArgs in = input_gradient(w, Bg, Bu, dA, M, N, K, p.splits_in, pieces);
+    const FfnArgs wt = weight_gradient(w, A, dBg, dBu, N, M, 2 * N, K, p.splits_w, pieces);
     return hip_status(run_gradients(dA && M > 0 ? &in : nullptr, dBg ? &wt : nullptr, s));
 }
 

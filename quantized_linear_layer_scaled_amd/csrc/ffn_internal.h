@@ -31,8 +31,6 @@ enum FfnEpi : int {
 struct FfnArgs {
     const uint8_t* P[2];
     const uint8_t* Q[2];
-    int64_t availP[2];  // bytes from P[i] to the end of its matrix
-    int64_t availQ[2];
     int64_t ldp, ldq;
     int C, R;
     int klen;      // elements of the contraction per segment
