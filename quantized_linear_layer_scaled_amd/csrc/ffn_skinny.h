@@ -9,12 +9,12 @@
 // wave order.  Past 16 rows a second block of tokens (TB = 2) meets the same
 // weight registers.  Measured and not kept (M = 1 to 16, N = 2048 to 12288): two
 // or four steps in flight per wave, 4 or 16 waves, two or four blocks of columns
-// per workgroup; each wins a few percent on some size and loses as much or
-// more on others (N = 2048, K = 6144, M = 4, bf16: 8.9 us, the others 8.8 to
-// 21; gated N = 12288, K = 4096, M = 1: 38.8 us = 5.2 TB/s, the others 35.8 to
-// 62).  The gated form puts 8 gate rows and 8 up rows in one 16-row block; the
-// linear form 16 rows, or 8 (the other half of the block stays zero) where 16
-// would leave compute units without a workgroup.
+// per workgroup; each wins up to 8% on some size and loses as much or more on
+// others (N = 2048, K = 6144, M = 4, bf16: 8.9 us, the others 8.8 to 21; gated
+// N = 12288, K = 4096, M = 1: 38.8 us = 5.2 TB/s, the others 35.8 to 62).  The
+// gated form puts 8 gate rows and 8 up rows in one 16-row block; the linear
+// form 16 rows, or 8 (the other half of the block stays zero) where 16 would
+// leave compute units without a workgroup.
 #pragma once
 
 #include "ffn_epilogue.h"

@@ -72,6 +72,15 @@ hipError_t ffn_launch(int fp8, int layout, int epi, FfnArgs a, hipStream_t strea
     return ffn_launch_reduce(a, stream);
 }
 
+// Up to 16 rows: this kernel / the tile (us, weights from HBM) at 1, 8 and 16
+// rows.  Linear bf16 N = 2048, K = 6144 10.8, 11.1, 12.0 / 12.0, 12.7, 12.9; FP8
+// the same 7.1, 7.2, 7.6 / 10.6, 11.0, 10.9; bf16 N = 12288, K = 4096 22.4, 22.3,
+// 27.5 / 26.1, 25.0, 25.0; FP8 the same 13.6, 13.8, 15.5 / 15.1, 15.2, 15.3.
+// Gated bf16 N = 2048, K = 6144 12.8, 13.3, 14.5 / 33.6, 33.8, 33.8; N = 4096,
+// K = 12288 38.4, 44.6, 55.3 / 64.4, 64.6, 64.8; FP8 N = 4096, K = 2048 5.8, 6.5,
+// 7.5 / 8.4, 8.4, 8.4.  It loses only near 16 rows with many weights, most for
+// gated N = 12288, K = 4096: bf16 38.0, 41.4, 52.8 / 44.1, 44.3, 44.4, FP8 19.1,
+// 22.6, 27.6 / 24.2, 24.3, 24.6.
 // From 17 rows on a workgroup here re-reads the tokens for every 8 or 16
 // columns, and the 64x64 tile for every 64 (gated 32), so the tile wins once the
 // weights are many.  Measured, this kernel / the tile (us) at 17 and 32 rows:
