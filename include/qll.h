@@ -406,7 +406,7 @@ int64_t qll_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   of quantize_per_token_fp8 (applied to the fp32 n).  n uses h unrounded.
  *   A row of n that holds a NaN has scale and codes NaN; one that holds an
  *   infinity (of w_pre) scale infinity, NaN codes there and zeros elsewhere.
- *   (A row whose squares sum to more than fp32 holds has rms infinity.)
+ *   A row whose squares sum to more than fp32 holds has rms infinity, n zero.
  *   y NULL: h = r (alpha 1, w_post, gate and r_out NULL).
  *   K % 8 == 0 (16 for e4m3), K <= 32768.  M == 0 is a no-op. */
 int residual_norm(const void* y, const void* r, int r_dtype, const void* w_post,
