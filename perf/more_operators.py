@@ -128,9 +128,10 @@ def prepare(case, seed):
     if case["op"] == "sample":
         B, V, ld = case["B"], case["V"], case["ld"]
         x = _normal(g, B, ld, std=2.0)
-        # a couple of dozen likely tokens a row
+        # a couple of dozen likely tokens a row, from hardly to far above the
+        # rest: an open question's distribution to a nearly certain one
         likely = torch.randint(0, V, (B, 24), generator=g, device=DEV)
-        x.scatter_(1, likely, 7.0 + _normal(g, B, 24, std=2.5))
+        x.scatter_(1, likely, 6.0 + 8.0 * _uniform(g, B, 1) + _normal(g, B, 24, std=2.5))
         s["logits"] = x.to(_type(case))[:, :V]
         s["u"] = _uniform(g, B)
         pick, a = _uniform(g, 4, B), _uniform(g, 4, B)
