@@ -130,7 +130,7 @@ def prepare(case, seed):
         x = _normal(g, B, ld, std=2.0)
         # a couple of dozen likely tokens a row, from hardly to far above the
         # rest: an open question's distribution to a nearly certain one
-        likely = torch.randint(0, V, (B, 24), generator=g, device=DEV)
+        likely = torch.randint(0, V // 24, (B, 24), generator=g, device=DEV) + V // 24 * torch.arange(24, device=DEV)
         x.scatter_(1, likely, 6.0 + 8.0 * _uniform(g, B, 1) + _normal(g, B, 24, std=2.5))
         s["logits"] = x.to(_type(case))[:, :V]
         s["u"] = _uniform(g, B)
