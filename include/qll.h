@@ -22,6 +22,12 @@
  *   gated_bf16, gated_fp8       gated projections, and the bf16 backward pass
  *   residual_norm               post-norm, gate, residual and pre-norm (bf16 or
  *                               e4m3 out), and the backward pass
+ *   moe_route, moe_sort         routing to experts (and the backward pass), rows
+ *                               sorted by expert
+ *   gated_fp8_grouped           the experts' gated projections, tokens gathered
+ *   moe_combine                 the weighted sum of the experts' outputs, and the
+ *                               backward pass
+ *   sample_tokens               temperature, top-k, top-p, min-p and the token
  * Each scaled GEMM runs as an ordinary tiled GEMM, as Split-K or as Swap-AB (the
  * three strategies of "What the integration changes"), chosen per (M, N, K)
  * by a dispatch table that an on-device sweep fills, or forced with the _ex
@@ -426,6 +432,130 @@ int residual_norm_backward(const void* y, const void* r, int r_dtype, const void
                            float* dw_post, float* dgate, float* dw_pre, int64_t M, int64_t K,
                            void* ws, size_t ws_bytes, void* stream);
 int64_t qll_residual_norm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* ------------------------------------------------------------------ */
+/* Experts                                                             */
+/* ------------------------------------------------------------------ */
+
+/* What stands around gemm_fp8_grouped in a mixture-of-experts layer.  T tokens
+ * choose topk of E experts each; the T * topk choices are sorted by expert into
+ * rows, which the grouped products run over, and the rows' outputs are joined
+ * again.  One layer, for x e4m3 [T][K] with scales sx:
+ *   moe_route(logits) -> ids, weights, offsets, rows, places
+ *   gated_fp8_grouped(x, gate, up, sx, .., offsets, rows) -> a [T * topk][N]
+ *   quantize_per_token_fp8(a) -> qa, sa
+ *   gemm_fp8_grouped(qa, down, sa, .., offsets) -> y [T * topk][K]
+ *   moe_combine(y, places, weights, residual) -> out [T][K]
+ * int32 and fp32 lists are 4-byte aligned, the rest 16-byte.  T * topk is at
+ * most 2^26, topk at most 64, E at most 1024 (UNSUPPORTED beyond). */
+typedef enum {
+    QLL_SCORE_SOFTMAX = 0, /* p = softmax(logits) over the experts */
+    QLL_SCORE_SIGMOID = 1  /* p = 1 / (1 + e^-logit) */
+} qll_score;
+
+/* Routing.  With c = p + bias, or the logits themselves without a bias:
+ *   groups: the experts come in `groups` runs of E / groups; a group's value is
+ *     the sum of its group_best (1 or 2) largest p + bias, and the topk_groups
+ *     groups of the largest values are open (all of them: topk_groups = groups)
+ *   ids[t][0..topk): the experts of open groups with the largest c, in falling
+ *     order; equal values go to the lower index, a NaN counts as -infinity
+ *   weights[t][j] = scale * p, with renormalize scale * p / (sum of p over the
+ *     chosen); the bias takes no part; 0 where that sum is 0
+ * c is formed in 64 bits, so values that differ are told apart.  A row of
+ * logits with a NaN or +infinity has NaN softmax weights (its ids are in range
+ * and distinct all the same); one of -infinity alone has softmax weights 0.
+ *   logits bf16 or fp32 [T][E] (logits_dtype, QLL_OUT_BF16 or _FP32); bias fp32
+ *   [E] or NULL; ids int32, weights fp32 [T][topk]; topk <= topk_groups * E /
+ *   groups; groups <= 64.
+ * offsets, rows and places: all NULL, or as moe_sort gives them for ids, with
+ * ws of qll_moe_sort_workspace_bytes(T, E, topk).
+ * T == 0 writes zeros to offsets. */
+int moe_route(const void* logits, int logits_dtype, const float* bias, int score, int64_t groups,
+              int64_t topk_groups, int group_best, int64_t topk, int renormalize, float scale,
+              int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* places,
+              int64_t T, int64_t E, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward pass: dlogits [T][E] (of the logits' type, every element
+ * written) for dweights fp32 [T][topk] at the chosen ids; the choice itself and
+ * the bias have no gradient.  An expert that ids names twice gets both terms;
+ * ids outside [0, E) have none. */
+int moe_route_backward(const void* logits, int logits_dtype, int score, int renormalize,
+                       float scale, const int32_t* ids, const float* dweights, void* dlogits,
+                       int64_t T, int64_t E, int64_t topk, void* stream);
+
+/* The choices sorted by expert, in the order of t * topk + j within one:
+ *   offsets int32 [E + 1]: expert e owns rows [offsets[e], offsets[e + 1])
+ *   rows int32 [T * topk]: the token of each row (choice / topk), -1 from
+ *     offsets[E] on
+ *   places int32 [T][topk]: the row of each choice, -1 for none
+ * ids int32 [T][topk]; one outside [0, E) (an expert of another device, say)
+ * has no row.  T == 0 writes zeros to offsets.
+ * ws: qll_moe_sort_workspace_bytes(T, E, topk) bytes (0 for up to 1024 choices). */
+int moe_sort(const int32_t* ids, int32_t* offsets, int32_t* rows, int32_t* places, int64_t T,
+             int64_t E, int64_t topk, void* ws, size_t ws_bytes, void* stream);
+int64_t qll_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t topk);
+
+/* The experts' gated projections, gated_fp8 with each row's own weights:
+ *   out[i][n] = act(g) u,  t = rows[i] (rows NULL: t = i, R = T),
+ *   g = (sum_k A[t][k] Bg[e][n][k]) sa[t] sg[e][n],  u likewise with Bu, su,
+ *   e the expert that owns row i
+ *   A e4m3 [T][K]; Bg, Bu e4m3 [E][N][K]; sa fp32 [T]; sg, su fp32 [E][N];
+ *   offsets int32 [E + 1], read as gemm_fp8_grouped reads them (rows that no
+ *   expert owns are left unwritten); rows int32 [R]: a token outside [0, T)
+ *   reads as zeros; out bf16 / fp32 [R][N].  K % 16 == 0, any N, E <= 65536.
+ *   With rows, T * K < 2^31 (UNSUPPORTED beyond, as are outputs of more tiles
+ *   than a launch holds, about R N = 2^35).  R == 0 is a no-op. */
+int gated_fp8_grouped(const void* A, const void* Bg, const void* Bu, const float* sa,
+                      const float* sg, const float* su, const int32_t* offsets,
+                      const int32_t* rows, int act, void* out, int out_dtype, int64_t T, int64_t R,
+                      int64_t N, int64_t K, int64_t E, void* stream);
+
+/* The join of the experts' outputs:
+ *   out[t] = residual[t] + sum_j weights[t][j] y[places[t][j]]
+ *   (fp32 sums, in the order of j; a place outside [0, R) adds nothing)
+ *   y bf16 [R][K]; places int32, weights fp32 [T][topk] (weights NULL: ones,
+ *   which sums the gradients of gathered tokens); residual of out's type or
+ *   NULL, may be out itself; out bf16 / fp32 [T][K].  K % 8 == 0. */
+int moe_combine(const void* y, const int32_t* places, const float* weights, const void* residual,
+                void* out, int out_dtype, int64_t T, int64_t R, int64_t K, int64_t topk,
+                void* stream);
+
+/* Its backward pass (the residual's gradient is dout itself):
+ *   dy[places[t][j]] = weights[t][j] dout[t],  dweights[t][j] = <dout[t], y[places[t][j]]>
+ *   dout bf16 / fp32 [T][K] (dout_dtype); dy bf16 [R][K] or NULL: rows that no
+ *   place names are left unwritten, and one that two places name holds either's;
+ *   dweights fp32 [T][topk] or NULL (needs y, else NULL; 0 without a row). */
+int moe_combine_backward(const void* y, const int32_t* places, const float* weights,
+                         const void* dout, int dout_dtype, void* dy, float* dweights, int64_t T,
+                         int64_t R, int64_t K, int64_t topk, void* stream);
+
+/* ------------------------------------------------------------------ */
+/* Sampling                                                            */
+/* ------------------------------------------------------------------ */
+
+/* One token per row of logits, behind a vocabulary projection.  With weights
+ * w_i = e^((logits[i] - max) / temperature) and the tokens in the order of
+ * falling logits, equal ones by rising index, these are kept:
+ *   1. the first top_k (off for values <= 0),
+ *   2. of them, those before which less than top_p of their weight lies (off
+ *      for values >= 1),
+ *   3. of them, those with w_i >= min_p (off for values <= 0),
+ * the first token always; the token is the first of the order up to which more
+ * than u of the kept tokens' weight lies, and probs its share of that weight.
+ * A temperature of 0, below or NaN takes the first token (probs 1).  NaN and
+ * -infinity are never chosen: a row of nothing else gives token -1, probs 0.
+ * A row with +infinity gives all of these the weight 1, the others none.
+ * Weights are formed in 64 bits; those below e^-32 are taken as 0.
+ *   logits bf16 or fp32 [B] rows of V values, `ld` values apart (ld >= V), of
+ *   their type's alignment; u fp32 [B] in [0, 1); temperature, top_p, min_p
+ *   fp32 [B], top_k int32 [B], each NULL for 1 or off; tokens int32 [B]; probs
+ *   fp32 [B] or NULL.  V <= 2^20 (UNSUPPORTED beyond), B < 2^22.
+ * ws: qll_sample_workspace_bytes(B, V).  B == 0 is a no-op. */
+int sample_tokens(const void* logits, int logits_dtype, int64_t ld, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p,
+                  const float* min_p, int32_t* tokens, float* probs, int64_t B, int64_t V,
+                  void* ws, size_t ws_bytes, void* stream);
+int64_t qll_sample_workspace_bytes(int64_t B, int64_t V);
 
 /* ------------------------------------------------------------------ */
 /* Without device allocation                                           */

@@ -21,7 +21,11 @@ Operations (see include/qll.h for the full contract):
   epilogue) and gemm_bf16_epilogue_backward,
   gated_bf16, gated_fp8 (act(x Bg^T) * (x Bu^T)) and gated_bf16_backward,
   residual_norm, residual_norm_backward (post-norm, gate, residual stream and
-  pre-norm in one pass).
+  pre-norm in one pass),
+  moe_route, moe_route_backward (routing to experts), moe_sort (rows sorted by
+  expert), gated_fp8_grouped (the experts' gated projections), moe_combine,
+  moe_combine_backward (the weighted sum of the experts' outputs),
+  sample_tokens (temperature, top-k, top-p, min-p and one token per row).
 """
 from __future__ import annotations
 
@@ -40,6 +44,7 @@ STATUS = {0: "QLL_OK", 1: "QLL_ERR_INVALID_ARG", 2: "QLL_ERR_UNSUPPORTED",
 OUT = {"bf16": 0, "fp32": 1, "int32": 2}
 OPS = {"int8": 0, "fp8": 1, "block_fp8": 2, "bf16_bi": 3, "mxfp4": 4, "w4a16": 5,
        "fp8_dynamic": 6}
+SCORE = {"softmax": 0, "sigmoid": 1}
 ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
 
 
@@ -114,6 +119,18 @@ def load_library():
     L.qll_gated_backward_workspace_bytes.argtypes = _MNK
     L.qll_residual_norm_backward_workspace_bytes.argtypes = [_I64, _I64]
     for name in ("epilogue", "epilogue_backward", "gated_backward", "residual_norm_backward"):
+        getattr(L, f"qll_{name}_workspace_bytes").restype = _I64
+    L.moe_route.argtypes = [_P, _I, _P, _I, _I64, _I64, _I, _I64, _I, _F] + [_P] * 5 + [_I64, _I64,
+                                                                                      _P, _Z, _P]
+    L.moe_route_backward.argtypes = [_P, _I, _I, _I, _F] + [_P] * 3 + _MNK + [_P]
+    L.moe_sort.argtypes = [_P] * 4 + _MNK + [_P, _Z, _P]
+    L.gated_fp8_grouped.argtypes = [_P] * 8 + [_I, _P, _I] + [_I64] * 5 + [_P]
+    L.moe_combine.argtypes = [_P] * 5 + [_I] + [_I64] * 4 + [_P]
+    L.moe_combine_backward.argtypes = [_P] * 4 + [_I, _P, _P] + [_I64] * 4 + [_P]
+    L.sample_tokens.argtypes = [_P, _I, _I64] + [_P] * 7 + [_I64, _I64, _P, _Z, _P]
+    L.qll_moe_sort_workspace_bytes.argtypes = _MNK
+    L.qll_sample_workspace_bytes.argtypes = [_I64, _I64]
+    for name in ("moe_sort", "sample"):
         getattr(L, f"qll_{name}_workspace_bytes").restype = _I64
     L.gemm_fp8_scaled_noalloc.argtypes = _GEMM_ARGS[:9] + [_P]
     L.qll_select.argtypes = [ctypes.c_int, _I64, _I64, _I64, ctypes.POINTER(qll_cfg)]
@@ -926,6 +943,273 @@ def residual_norm_backward(y, r, w_pre, dn, dr_out=None, w_post=None, gate=None,
     if rc:
         raise QllError("residual_norm_backward", rc)
     return dy, dr, dw_pre, dw_post, dgate
+
+
+# --------------------------------------------------------------------------
+# experts
+# --------------------------------------------------------------------------
+
+def _choices(t, name):
+    shape = _matrix(t, name)
+    if shape[1] < 1:
+        raise ValueError(f"{name} must have a column per choice")
+    return shape
+
+
+def _bf16_or_f32(t, name):
+    """0 or 1, the code of the tensor's type."""
+    torch = _torch()
+    dt = getattr(t, "dtype", None)
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float32:
+        return 1
+    raise ValueError(f"{name} must be bfloat16 or float32")
+
+
+def _score(score):
+    code = SCORE.get(score)
+    if code is None:
+        raise ValueError(f"unknown score {score!r}: one of {', '.join(SCORE)}")
+    return code
+
+
+def _given(t, name, dtype, shape, like, here):
+    """(tensor, its pointer), allocated if not given."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _need(t, name, dtype, shape, here)
+
+
+def _plan(T, E, topk, offsets, rows, places, workspace, like, here, L):
+    """(offsets, rows, places, their pointers, workspace arguments)"""
+    i32 = _torch().int32
+    offsets, po = _given(offsets, "offsets", i32, (E + 1,), like, here)
+    rows, pr = _given(rows, "rows", i32, (T * topk,), like, here)
+    places, pp = _given(places, "places", i32, (T, topk), like, here)
+    ws = _scratch("qll_moe_sort_workspace_bytes", L.qll_moe_sort_workspace_bytes(T, E, topk),
+                  workspace, like, here)
+    return offsets, rows, places, (po, pr, pp), ws
+
+
+def moe_route(logits, topk, score="softmax", bias=None, groups=1, topk_groups=None, group_best=2,
+              renormalize=True, scale=1.0, plan=False, ids=None, weights=None, offsets=None,
+              rows=None, places=None, workspace=None, stream=None):
+    """(ids int32 [T][topk], weights fp32 [T][topk]) of bf16 or fp32 router
+    logits [T][E]: the topk experts of each token by softmax or sigmoid score
+    (+ fp32 bias [E]), from the topk_groups best of `groups` groups (None: all
+    of them), and their scores, renormalised or not, times scale.  With plan
+    also what moe_sort gives: (ids, weights, offsets, rows, places)."""
+    if stream is not None:
+        return _under(stream, moe_route, logits, topk, score, bias, groups, topk_groups, group_best,
+                      renormalize, scale, plan, ids, weights, offsets, rows, places, workspace)
+    torch = _torch()
+    here, st = _place()
+    T, E = _matrix(logits, "logits")
+    kind, code = _bf16_or_f32(logits, "logits"), _score(score)
+    if not plan and (offsets is not None or rows is not None or places is not None):
+        raise ValueError("offsets, rows and places need plan")
+    if topk < 1:
+        raise ValueError("topk must be 1 or more")
+    L = load_library()
+    pl, pb = _need(logits, "logits", logits.dtype, (T, E), here), _arg(bias, "bias", torch.float32,
+                                                                      (E,), here)
+    ids, pi = _given(ids, "ids", torch.int32, (T, topk), logits, here)
+    weights, pw = _given(weights, "weights", torch.float32, (T, topk), logits, here)
+    lists, ws, wsb = (None, None, None), None, 0
+    if plan:
+        offsets, rows, places, lists, (ws, wsb, keep) = _plan(T, E, topk, offsets, rows, places,
+                                                              workspace, logits, here, L)
+    rc = L.moe_route(pl, kind, pb, code, groups, groups if topk_groups is None else topk_groups,
+                     group_best, topk, renormalize, scale, pi, pw, *lists, T, E, ws, wsb, st)
+    if rc:
+        raise QllError("moe_route", rc)
+    return (ids, weights, offsets, rows, places) if plan else (ids, weights)
+
+
+def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0,
+                       dlogits=None, stream=None):
+    """dlogits [T][E], of the logits' type, of moe_route for fp32 dweights
+    [T][topk] at int32 ids [T][topk]."""
+    if stream is not None:
+        return _under(stream, moe_route_backward, logits, ids, dweights, score, renormalize, scale,
+                      dlogits)
+    torch = _torch()
+    here, st = _place()
+    T, E = _matrix(logits, "logits")
+    kind, code = _bf16_or_f32(logits, "logits"), _score(score)
+    topk = _choices(ids, "ids")[1]
+    lead = (_need(logits, "logits", logits.dtype, (T, E), here), kind, code, renormalize, scale,
+            _need(ids, "ids", torch.int32, (T, topk), here),
+            _need(dweights, "dweights", torch.float32, (T, topk), here))
+    dlogits, pd = _given(dlogits, "dlogits", logits.dtype, (T, E), logits, here)
+    rc = load_library().moe_route_backward(*lead, pd, T, E, topk, st)
+    if rc:
+        raise QllError("moe_route_backward", rc)
+    return dlogits
+
+
+def moe_sort(ids, experts, offsets=None, rows=None, places=None, workspace=None, stream=None):
+    """(offsets int32 [experts + 1], rows int32 [T * topk], places int32
+    [T][topk]) of int32 ids [T][topk]: the choices sorted by expert, the token
+    of each sorted row and the row of each choice; -1 for an id that is none
+    of the experts and for the rows behind the last choice."""
+    if stream is not None:
+        return _under(stream, moe_sort, ids, experts, offsets, rows, places, workspace)
+    here, st = _place()
+    T, topk = _choices(ids, "ids")
+    L = load_library()
+    pi = _need(ids, "ids", _torch().int32, (T, topk), here)
+    if experts < 1:
+        raise ValueError("experts must be 1 or more")
+    offsets, rows, places, lists, (ws, wsb, keep) = _plan(T, experts, topk, offsets, rows, places,
+                                                          workspace, ids, here, L)
+    rc = L.moe_sort(pi, *lists, T, experts, topk, ws, wsb, st)
+    if rc:
+        raise QllError("moe_sort", rc)
+    return offsets, rows, places
+
+
+def _expert_codes(t, name, shape, here):
+    """Pointer of e4m3 codes [E][N][K]: float8_e4m3fn, or their bytes."""
+    if shape is None or len(shape) != 3:
+        raise ValueError(f"{name} must be a 3-D tensor")
+    return _codes(t, name, shape, here)
+
+
+def gated_fp8_grouped(A, Bg, Bu, sa, sg, su, offsets, rows=None, act="silu", out_dtype="bf16",
+                      out=None, stream=None):
+    """act((x Bg[e]^T) sa sg[e]) * ((x Bu[e]^T) sa su[e]) of every row i, x =
+    A[rows[i]] (rows None: A[i]), e the expert that owns row i: e4m3 A [T][K],
+    Bg and Bu [E][N][K], fp32 sa [T], sg and su [E][N], int32 offsets [E + 1]
+    and rows [R] on the GPU.  Rows that no expert owns are left unwritten."""
+    if stream is not None:
+        return _under(stream, gated_fp8_grouped, A, Bg, Bu, sa, sg, su, offsets, rows, act,
+                      out_dtype, out)
+    torch = _torch()
+    here, st = _place()
+    T, K = _matrix(A, "A")
+    shape = getattr(Bg, "shape", (0, 0, 0))
+    pg = _expert_codes(Bg, "Bg", (*shape[:2], K) if len(shape) == 3 else None, here)
+    E, N = shape[:2]
+    i32, f32 = torch.int32, torch.float32
+    if rows is None:
+        R, pr = T, None
+    else:
+        if getattr(rows, "ndim", 1) != 1:
+            raise ValueError("rows must be a 1-D tensor")
+        R = rows.numel() if isinstance(rows, torch.Tensor) else 0
+        pr = _need(rows, "rows", i32, (R,), here)
+    lead = (_codes(A, "A", (T, K), here), pg, _expert_codes(Bu, "Bu", (E, N, K), here),
+            _scales(sa, "sa", T, here), _need(sg, "sg", f32, (E, N), here),
+            _need(su, "su", f32, (E, N), here), _need(offsets, "offsets", i32, (E + 1,), here), pr,
+            _act(act))
+    out, po, od = _float_out(out, R, N, out_dtype, A, here)
+    rc = load_library().gated_fp8_grouped(*lead, po, od, T, R, N, K, E, st)
+    if rc:
+        raise QllError("gated_fp8_grouped", rc)
+    return out
+
+
+def moe_combine(y, places, weights=None, residual=None, out_dtype=None, out=None, stream=None):
+    """residual + sum_j weights[:, j] y[places[:, j]]: bf16 y [R][K], int32
+    places [T][topk], fp32 weights [T][topk] (None: ones), residual [T][K] of
+    the output's type.  out_dtype None: the residual's type, else bf16."""
+    if stream is not None:
+        return _under(stream, moe_combine, y, places, weights, residual, out_dtype, out)
+    torch = _torch()
+    here, st = _place()
+    R, K = _matrix(y, "y")
+    T, topk = _choices(places, "places")
+    if out_dtype is None:
+        out_dtype = ("bf16", "fp32")[_bf16_or_f32(residual, "residual")] if residual is not None \
+            else "bf16"
+    py = _need(y, "y", torch.bfloat16, (R, K), here)
+    pp = _need(places, "places", torch.int32, (T, topk), here)
+    pw = _arg(weights, "weights", torch.float32, (T, topk), here)
+    out, po, od = _float_out(out, T, K, out_dtype, y, here)
+    pr = _arg(residual, "residual", out.dtype, (T, K), here)
+    rc = load_library().moe_combine(py, pp, pw, pr, po, od, T, R, K, topk, st)
+    if rc:
+        raise QllError("moe_combine", rc)
+    return out
+
+
+def moe_combine_backward(y, places, weights, dout, need_y=True, need_weights=True, dy=None,
+                         dweights=None, stream=None):
+    """(dy, dweights) of moe_combine for dout bf16 or fp32 [T][K] (the
+    residual's gradient is dout itself): dy bf16 [R][K], whose rows that no
+    place names are left unwritten, dweights fp32 [T][topk]; None for what is
+    not needed, and for dweights without weights."""
+    if stream is not None:
+        return _under(stream, moe_combine_backward, y, places, weights, dout, need_y, need_weights,
+                      dy, dweights)
+    torch = _torch()
+    here, st = _place()
+    R, K = _matrix(y, "y")
+    T, topk = _choices(places, "places")
+    need_weights = need_weights and weights is not None
+    if not (need_y or need_weights):
+        raise ValueError("nothing to compute")
+    bf, f32 = torch.bfloat16, torch.float32
+    kind = _bf16_or_f32(dout, "dout")
+    lead = (_need(y, "y", bf, (R, K), here), _need(places, "places", torch.int32, (T, topk), here),
+            _arg(weights, "weights", f32, (T, topk), here), _need(dout, "dout", dout.dtype, (T, K), here),
+            kind)
+    pdy = pdw = None
+    if need_y:
+        dy, pdy = _given(dy, "dy", bf, (R, K), y, here)
+    else:
+        dy = None
+    if need_weights:
+        dweights, pdw = _given(dweights, "dweights", f32, (T, topk), y, here)
+    else:
+        dweights = None
+    rc = load_library().moe_combine_backward(*lead, pdy, pdw, T, R, K, topk, st)
+    if rc:
+        raise QllError("moe_combine_backward", rc)
+    return dy, dweights
+
+
+# --------------------------------------------------------------------------
+# sampling
+# --------------------------------------------------------------------------
+
+def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=False,
+                  tokens=None, workspace=None, stream=None):
+    """int32 tokens [B], one per row of bf16 or fp32 logits [B][V] (rows may be
+    padded: any row stride), from fp32 random numbers u [B] in [0, 1), by
+    temperature, top_p, min_p fp32 [B] and top_k int32 [B] (None: 1, or off).
+    probs: True, or an fp32 [B] tensor to fill, returns (tokens, probs) with
+    each token's share of the kept weight."""
+    if stream is not None:
+        return _under(stream, sample_tokens, logits, u, temperature, top_k, top_p, min_p, probs,
+                      tokens, workspace)
+    torch = _torch()
+    here, st = _place()
+    B, V = _matrix(logits, "logits")
+    kind = _bf16_or_f32(logits, "logits")
+    if not logits.is_cuda or logits.get_device() != here:
+        _refuse(logits, "logits", "on the GPU", here)
+    ld = logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError("the values of a row of logits must be contiguous, the rows apart")
+    f32, i32 = torch.float32, torch.int32
+    lead = (logits.data_ptr(), kind, ld, _need(u, "u", f32, (B,), here),
+            _arg(temperature, "temperature", f32, (B,), here), _arg(top_k, "top_k", i32, (B,), here),
+            _arg(top_p, "top_p", f32, (B,), here), _arg(min_p, "min_p", f32, (B,), here))
+    L = load_library()
+    tokens, pt = _given(tokens, "tokens", i32, (B,), u, here)
+    share, pp = None, None
+    if probs is not False and probs is not None:
+        share, pp = _given(None if probs is True else probs, "probs", f32, (B,), u, here)
+    ws, wsb, keep = _scratch("qll_sample_workspace_bytes", L.qll_sample_workspace_bytes(B, V),
+                             workspace, u, here)
+    rc = L.sample_tokens(*lead, pt, pp, B, V, ws, wsb, st)
+    if rc:
+        raise QllError("sample_tokens", rc)
+    return tokens if share is None else (tokens, share)
 
 
 # --------------------------------------------------------------------------

@@ -206,7 +206,7 @@ struct ColumnVector {
 template <int EPI, int W>
 __device__ __forceinline__ void load_columns(const FfnArgs& a, int c, ColumnVector<W>& v)
 {
-    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_DZ) {
+    if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_DZ || EPI == EPI_GROUPED) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             v.s0[i] = v.s1[i] = v.b[i] = 0.0f;
@@ -214,13 +214,20 @@ __device__ __forceinline__ void load_columns(const FfnArgs& a, int c, ColumnVect
                 continue;
             if (EPI != EPI_DZ && a.sq) {
                 v.s0[i] = a.sp[0][c + i];
-                if (EPI == EPI_GATED)
+                if (EPI == EPI_GATED || EPI == EPI_GROUPED)
                     v.s1[i] = a.sp[1][c + i];
             }
-            if (EPI != EPI_GATED && a.bias)
+            if (EPI != EPI_GATED && EPI != EPI_GROUPED && a.bias)
                 v.b[i] = bf16_value(a.bias[c + i]);
         }
     }
+}
+
+// The scale of a row whose token is looked up; a row of no token has none.
+__device__ __forceinline__ float grouped_scale(const FfnArgs& a, int r)
+{
+    const int t = a.rows ? a.rows[r] : r;
+    return (unsigned)t < (unsigned)a.tokens ? a.sq[t] : 0.0f;
 }
 
 // The W output columns c .. c + W - 1 of row r, whose fp32 sums are v (gated:
@@ -247,8 +254,8 @@ __device__ __forceinline__ void ffn_store_act(const FfnArgs& a, float* v, const 
     } else if constexpr (EPI == EPI_PLAIN) {
         uint16_t* base = (uint16_t*)(r < a.row_split ? a.out : a.out2);
         store_bf16<W>(base + (size_t)(r < a.row_split ? r : r - a.row_split) * a.ldo + c, v);
-    } else if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED) {
-        const float s = a.sq ? a.sq[r] : 1.0f;
+    } else if constexpr (EPI == EPI_LINEAR || EPI == EPI_GATED || EPI == EPI_GROUPED) {
+        const float s = EPI == EPI_GROUPED ? grouped_scale(a, r) : (a.sq ? a.sq[r] : 1.0f);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float z = v[i];

@@ -19,7 +19,8 @@ enum FfnEpi : int {
     EPI_DZ,          // out = dy * act'(sum + bias[c]), column sums of out to `partial`
     EPI_DGATED,      // out[r][c] = dy * u * act'(g), out[r][C + c] = dy * act(g)
     EPI_PLAIN,       // out = sum (rows from row_split on to out2)
-    EPI_PARTIAL      // Split-K: fp32 sums to `partial` [split][R][C]
+    EPI_PARTIAL,     // Split-K: fp32 sums to `partial` [split][R][C]
+    EPI_GROUPED      // EPI_GATED, the scale of row r being sq[rows[r]]
 };
 
 // out[r][c] = epilogue(sum_k Q[r][k] P[c][k]).  P holds the operand along the
@@ -45,6 +46,8 @@ struct FfnArgs {
     int out_fp32;
     int act;
     const float* sq;        // [R]: FP8 scales of the rows
+    const int* rows;        // EPI_GROUPED: [R] or null (r itself)
+    int tokens;             // entries of sq there
     const float* sp[2];     // [C]: FP8 scales of the columns
     const uint16_t* bias;   // bf16 [C] or null
     const uint16_t* res;    // bf16 [R][C] or null
