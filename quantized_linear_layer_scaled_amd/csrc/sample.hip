@@ -9,24 +9,29 @@
 //
 // Every set of that definition is a front part of one order, so a row needs
 // no sorting: only where in the order a count, a weight or a value is reached.
-// A workgroup takes a row.  One pass finds the maximum; a second one puts
-// every value into one of kBins bins of d, 1 / kPerUnit wide, by one LDS
-// addition that carries a count and a weight; prefix sums over the bins then
-// say in which bin an answer lies, and a third pass gathers the few values of
-// that bin, or of all bins up to it where these are few too, which is the usual
-// case with top-k or a peaked distribution; they are sorted in LDS.
+// A row is read once.  Its values go to one of kBins bins of
+// (ref - x) / T, 1 / kPerUnit wide, each by one LDS addition that carries a
+// count and a weight, and those among the largest also to a list; ref and the
+// list's threshold come from a sample of the row.  Prefix sums over the bins
+// say in which bin an answer lies.  Mostly (top-k, a peaked distribution) the
+// list holds all values down to there; they are sorted and added up one by one.
+// Else a second pass gathers the bins that matter.
 //
 // A token is right or wrong, so weights are formed to well below a token's
 // share: within a bin w = e^-(b / kPerUnit) (1 - g), g = 1 - e^-(f / kPerUnit)
-// with f the fraction of the bin (64-bit arithmetic, four terms: 2^-42), and
+// with f the fraction of the bin (64-bit arithmetic, four terms: 2^-37), and
 // the additions are integers: the count above, g in `ebits` fractional bits
-// below (35 for vocabularies below 2^18), which no order of additions changes.
+// below (34 for vocabularies below 2^18), which no order of additions changes.
 // Weights below e^-32 of the largest are left out: 2^20 of them are less than
 // 1.4e-8 of the total, below the last bit of u next to 1 (6e-8).
 //
-// A bin that holds more values than the list (equal logits, a wide
-// temperature) is narrowed down by further passes over its keys, 4096 ways
-// each; equal keys are counted by blocks of the row.
+// The bins cover 16 T above ref and 32 T below; a row whose maximum lies above
+// starts again with ref = the maximum.  A bin that holds more values than the
+// list (equal logits, a wide temperature) is narrowed down by further passes
+// over its keys, 4096 ways each; equal keys are counted by blocks of the row.
+//
+// A workgroup takes a row, or one of `parts` of it where there are few rows;
+// then a second launch adds the parts' bins and finishes.
 #include "ffn_epilogue.h"
 #include "sample_internal.h"
 
@@ -36,10 +41,32 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 4096;
-constexpr int kPerUnit = 128;  // bins per unit of d
-constexpr int kCap = 4096;     // values in the list
+constexpr int kBins = 3072;
+constexpr int kPerUnit = 64;             // bins per unit of (ref - x) / T
+constexpr int kPer = kBins / kThreads;   // bins of a thread
+// the bin of ref, 16 units above (a thread's first, whose weight at ref is
+// exactly 1: equal weights stay equal)
+constexpr int kAbove = 16 * kPerUnit / kPer * kPer + kPer;
+constexpr int kCap = 4096;               // values that are kept beside the bins
+constexpr int kFew = 256;                // values that are sorted
+constexpr int kSub = 4096;               // ways a bin is narrowed down
 constexpr float kInf = __builtin_inff();
+constexpr float kMax = 3.402823466e38f;
+
+// A value that is the same in every lane, in scalar registers: the row's
+// numbers would take most of the vector registers.
+template <typename T>
+__device__ __forceinline__ T uniform(T v)
+{
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+        const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(u >> 32));
+        return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+    }
+}
 
 // Unsigned numbers in the order of the values; NaN as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float v)
@@ -52,80 +79,139 @@ __device__ __forceinline__ float value_of(uint32_t key)
 {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
+__device__ __forceinline__ uint64_t entry(float x, int i)
+{
+    return ((uint64_t)~key_of(x) << 32) | (uint32_t)i;
+}
+__device__ __forceinline__ uint32_t entry_key(uint64_t e) { return ~(uint32_t)(e >> 32); }
+
+// What a part of a row leaves for the second launch.
+struct Part {
+    uint64_t bins[kBins];
+    uint64_t list[kSamplePartList];
+    uint32_t n;  // values for the list (more than it holds: not all are there)
+    float max;
+    float ref, threshold;
+};
 
 struct Shared {
-    uint64_t bins[kBins];      // then: weight before each bin, as doubles
+    uint64_t bins[kBins];        // then: weight before each bin, as doubles
     uint32_t counts[kBins + 1];  // values before each bin
-    uint64_t list[kCap];       // ~key, index
-    double sums[kCap];         // weight up to and with each list entry
+    uint64_t cand[kCap];         // values of some bins
+    uint64_t list[kSub];         // few values, sorted, or the finer bins of a search
+    double sums[kFew];           // weight up to and with each of these
     double wave_weight[kWaves];
     uint32_t wave_count[kWaves];
     float wave_max[kWaves];
-    uint32_t n;
-    int index;
+    uint32_t n, ncand;
+    int found, last, index;
 };
 
 // A place in the order.
 struct Place {
     uint32_t key;
-    int index;      // of the token, or -1 where nobody asked for it
+    int index;      // of the token, or -1: it is the rank-th with this key
+    int rank;       // (from 1)
     double weight;  // of one value
     double upto;    // weight up to and with this place
 };
 
+// Values of a row, 16 bytes at a time.
 template <bool BF16>
 struct Row {
+    static constexpr int VE = BF16 ? 8 : 4;
     const void* p;
     int V;
-    // f(value, index) for all values
-    template <typename F>
-    __device__ __forceinline__ void each(F&& f) const
+
+    __device__ __forceinline__ int vectors() const { return V / VE; }
+    __device__ __forceinline__ u32x4_any load(int v) const
     {
-        constexpr int VE = BF16 ? 8 : 4;
-        constexpr int U = 4;
-        const int nv = V / VE;
-        for (int v0 = threadIdx.x; v0 < nv; v0 += U * kThreads) {
-            u32x4_any w[U];
+        return *(const u32x4_any*)((const char*)p + (size_t)v * 16);
+    }
+    static __device__ __forceinline__ void widen(const u32x4_any& w, float (&x)[VE])
+    {
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (v0 + k * kThreads < nv)
-                    w[k] = *(const u32x4_any*)((const char*)p + (size_t)(v0 + k * kThreads) * 16);
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int at = (v0 + k * kThreads) * VE;
-                if (v0 + k * kThreads < nv) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        float x;
-                        if constexpr (BF16)
-                            x = __uint_as_float(e & 1 ? w[k][e / 2] & 0xFFFF0000u : w[k][e / 2] << 16);
-                        else
-                            x = __uint_as_float(w[k][e]);
-                        f(x, at + e);
-                    }
-                }
-            }
+        for (int e = 0; e < VE; ++e) {
+            if constexpr (BF16)
+                x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+            else
+                x[e] = __uint_as_float(w[e]);
         }
-        const int i = nv * VE + (int)threadIdx.x;
-        if (i < V)
-            f(at(i), i);
     }
     __device__ __forceinline__ float at(int i) const
     {
         return BF16 ? bf16_value(((const uint16_t*)p)[i]) : ((const float*)p)[i];
     }
+    // f(values, index of the first, how many) for vectors v0 .. v1 - 1, and
+    // the values behind the last whole vector where `tail`
+    template <typename F>
+    __device__ __forceinline__ void each(int v0, int v1, bool tail, F&& f) const
+    {
+        // (the next vectors are loaded before these are used)
+        constexpr int U = 16 / VE;
+        int v = v0 + (int)threadIdx.x;
+        u32x4_any next[U];
+        if (v < v1) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                next[k] = load(min(v + k * kThreads, v1 - 1));
+        }
+        for (; v < v1; v += U * kThreads) {
+            u32x4_any w[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                w[k] = next[k];
+            if (v + U * kThreads < v1) {
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    next[k] = load(min(v + (U + k) * kThreads, v1 - 1));
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                float x[VE];
+                widen(w[k], x);
+                if (v + k * kThreads < v1)
+                    f(x, (v + k * kThreads) * VE);
+            }
+        }
+        const int i = vectors() * VE + (int)threadIdx.x;
+        if (tail && i < V) {
+            float x[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                x[e] = -kInf;
+            x[0] = at(i);
+            f(x, i);
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F&& f) const
+    {
+        each(0, vectors(), true, f);
+    }
 };
 
 // The order of a row's weights.
 struct Scale {
-    double max, per;  // d * kPerUnit = (max - x) * per
-    double inv_t;
-    double one;  // 2^ebits
-    int shift;   // of the count
+    double ref, per;  // bins: (ref - x) per + kAbove
+    double one;       // 2^ebits
+    double top;       // steps(maximum): the place of weight 1
+    int shift;        // of the count
 
-    __device__ __forceinline__ double steps(float x) const { return (max - (double)x) * per; }
-    // the bin of a value, -1 for none; y: steps(x)
-    __device__ __forceinline__ int bin(double y) const { return y < (double)kBins ? (int)y : -1; }
+    __device__ __forceinline__ double steps(float x) const
+    {
+        return __builtin_fma(ref - (double)x, per, (double)kAbove);
+    }
+    static __device__ __forceinline__ bool inside(double y)
+    {
+        return fabs(y - kBins / 2) < kBins / 2;  // (0 is outside)
+    }
+    // the bin of a value, -1 for none
+    __device__ __forceinline__ int bin(float x) const
+    {
+        const double y = steps(x);
+        return inside(y) ? (int)y : -1;
+    }
     // what a value adds to its bin
     __device__ __forceinline__ uint64_t share(double y) const
     {
@@ -140,16 +226,52 @@ struct Scale {
         return (uint64_t)(uint32_t)__builtin_bit_cast(uint64_t, q) | (1ull << shift);
     }
     __device__ __forceinline__ uint32_t count(uint64_t sum) const { return (uint32_t)(sum >> shift); }
-    __device__ __forceinline__ double weight(uint64_t sum, int bin) const
+    // a bin's weight over that of its upper end
+    __device__ __forceinline__ double part(uint64_t sum) const
     {
-        const double g = (double)(sum & ((1ull << shift) - 1)) / one;
-        return ((double)count(sum) - g) * exp(-(double)bin / kPerUnit);
+        return (double)count(sum) - (double)(sum & ((1ull << shift) - 1)) / one;
+    }
+    __device__ __forceinline__ double weight_at(double y) const
+    {
+        return exp((top - y) * (1.0 / kPerUnit));
     }
     __device__ __forceinline__ double weight(uint32_t key) const
     {
-        return exp(-(max - (double)value_of(key)) * inv_t);
+        return weight_at(steps(value_of(key)));
     }
 };
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, ((uint64_t)dpp<CTRL, ROWS>((uint32_t)(u >> 32)) << 32) |
+                                          dpp<CTRL, ROWS>((uint32_t)u));
+}
+// Inclusive prefix sums over a wave.
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v)
+{
+    v += dpp<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += dpp<0x112, 0xF>(v);
+    v += dpp<0x114, 0xF>(v);
+    v += dpp<0x118, 0xF>(v);
+    v += dpp<0x142, 0xA>(v);  // row_bcast 15, 31
+    v += dpp<0x143, 0xC>(v);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        v = fmaxf(v, __shfl_xor(v, d, 64));
+    return v;
+}
 
 // Exclusive prefix sums of a count and a weight over the threads; the totals
 // go to every thread.
@@ -157,21 +279,14 @@ __device__ __forceinline__ void scan_threads(Shared& s, uint32_t& count, double&
                                              uint32_t& all, double& total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t c = count;
-    double w = weight;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t oc = __shfl_up(c, d, 64);
-        const double ow = __shfl_up(w, d, 64);
-        if (lane >= d) {
-            c += oc;
-            w += ow;
-        }
-    }
+    const uint32_t c = wave_scan(count);
+    const double w = wave_scan(weight);
     if (lane == 63) {
         s.wave_count[wave] = c;
         s.wave_weight[wave] = w;
     }
+    // (the sum before a lane is its neighbour's, not a difference: that would
+    // round)
     const uint32_t before_c = __shfl_up(c, 1, 64);
     const double before_w = __shfl_up(w, 1, 64);
     __syncthreads();
@@ -208,136 +323,357 @@ __device__ __forceinline__ int first_of(int n, F&& past)
     return lo;
 }
 
-// Sorts the n values of the list: a bitonic network.
-__device__ void sort_list(Shared& s, int n)
-{
-    int size = 1;
-    while (size < n)
-        size <<= 1;
-    for (int i = n + (int)threadIdx.x; i < size; i += kThreads)
-        s.list[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                const int i = 2 * t - (t & (j - 1));
-                const uint64_t a = s.list[i], b = s.list[i + j];
-                if ((a > b) == ((i & k) == 0)) {
-                    s.list[i] = b;
-                    s.list[i + j] = a;
-                }
-            }
-            __syncthreads();
-        }
-}
-
 template <bool BF16>
 struct Sampler {
     Shared& s;
     const Row<BF16> row;
     Scale scale;
+    double total;  // weight of all bins
+    uint32_t all;  // their values
+    int lo[2], hi[2];  // cand holds the bins lo[i] .. hi[i]
 
-    __device__ __forceinline__ uint32_t list_key(int i) const { return ~(uint32_t)(s.list[i] >> 32); }
-
-    // Values with a key in [lo, hi] and a bin in [b0, b1] to the list.
-    __device__ int gather(int b0, int b1, uint32_t lo, uint32_t hi)
+    // ref and the list's threshold from a sample: 16 values of every thread,
+    // from four places of the row.  The threshold is the least of the waves'
+    // maxima, each of 1024 values: about 1 in 370 values lies above.
+    __device__ __forceinline__ void sample(float& ref, float& threshold)
     {
+        constexpr int S = 16 / Row<BF16>::VE;
+        const int nv = row.vectors();
+        const int chunk = kThreads / 4;
+        const int quarter = max(nv / 4, 1);
+        float m = -kInf;
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const int v = (int)(threadIdx.x / chunk) * quarter + k * chunk + (int)(threadIdx.x % chunk);
+            if (k * chunk + (int)(threadIdx.x % chunk) < quarter && v < nv) {
+                float x[Row<BF16>::VE];
+                Row<BF16>::widen(row.load(v), x);
+#pragma unroll
+                for (int e = 0; e < Row<BF16>::VE; ++e)
+                    m = fmaxf(m, x[e]);
+                any = true;
+            }
+        }
+        m = wave_max(m);
+        any = __any(any);
+        if ((threadIdx.x & 63) == 0)
+            s.wave_max[threadIdx.x >> 6] = any ? m : kInf;
+        __syncthreads();
+        ref = -kInf;
+        threshold = kInf;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float v = s.wave_max[w];
+            threshold = fminf(threshold, v);
+            ref = v < kInf ? fmaxf(ref, v) : ref;
+        }
+        ref = uniform(ref);
+        threshold = uniform(threshold == kInf ? -kMax : fmaxf(threshold, -kMax));
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ void clear_bins()
+    {
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+            s.bins[i] = 0;
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ void keep(float x, int i)
+    {
+        const uint32_t to = atomicAdd(&s.ncand, 1u);
+        if (to < kCap)
+            s.cand[to] = entry(x, i);
+    }
+
+    // Vectors v0 .. v1 - 1 to the bins (where `binned`), values from the
+    // threshold on to cand; returns the workgroup's maximum.
+    __device__ __forceinline__ float stream(int v0, int v1, bool tail, bool binned, float threshold)
+    {
+        constexpr int VE = Row<BF16>::VE;
+        float m = -kInf;
+        row.each(v0, v1, tail, [&](const float (&x)[VE], int i) {
+            float most = x[0];
+#pragma unroll
+            for (int e = 1; e < VE; ++e)
+                most = fmaxf(most, x[e]);
+            m = fmaxf(m, most);
+            if (binned) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const double y = scale.steps(x[e]);
+                    if (Scale::inside(y))
+                        atomicAdd((unsigned long long*)&s.bins[(int)y],
+                                  (unsigned long long)scale.share(y));
+                }
+            }
+            if (most >= threshold) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (x[e] >= threshold)
+                        keep(x[e], i + e);
+            }
+        });
+        m = wave_max(m);
+        if ((threadIdx.x & 63) == 0)
+            s.wave_max[threadIdx.x >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            m = fmaxf(m, s.wave_max[w]);
+        return uniform(m);
+    }
+
+    // The bins to prefix sums.
+    __device__ __forceinline__ void scan_bins()
+    {
+        double* before = (double*)s.bins;
+        uint32_t c = 0, mine_c[kPer];
+        double w = 0.0, mine_w[kPer];
+        double e = scale.weight_at((double)(threadIdx.x * kPer));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint64_t v = s.bins[threadIdx.x * kPer + i];
+            mine_c[i] = scale.count(v);
+            mine_w[i] = scale.part(v) * e;
+            e *= 0.9844964370054085;  // e^(-1 / kPerUnit)
+            c += mine_c[i];
+            w += mine_w[i];
+        }
+        scan_threads(s, c, w, all, total);
+        all = uniform(all);
+        total = uniform(total);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            s.counts[threadIdx.x * kPer + i] = c;
+            before[threadIdx.x * kPer + i] = w;
+            if (mine_c[i] && c + mine_c[i] == all)
+                s.last = threadIdx.x * kPer + i;
+            c += mine_c[i];
+            w += mine_w[i];
+        }
+        if (threadIdx.x == 0)
+            s.counts[kBins] = all;
+        __syncthreads();
+    }
+    __device__ __forceinline__ double weight_before(int b) const
+    {
+        return b < kBins ? ((const double*)s.bins)[b] : total;
+    }
+    __device__ __forceinline__ uint32_t count_in(int b0, int b1) const
+    {
+        return s.counts[b1 + 1] - s.counts[b0];
+    }
+
+    // The first bin up to which past(count, weight) holds, else the last that
+    // holds values.
+    template <typename F>
+    __device__ __forceinline__ int bin_by(F&& past)
+    {
+        if (threadIdx.x == 0)
+            s.found = -1;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = threadIdx.x * kPer + i;
+            const uint32_t c0 = s.counts[b], c1 = s.counts[b + 1];
+            if (c1 > c0 && past(c1, weight_before(b + 1)) && (c0 == 0 || !past(c0, weight_before(b))))
+                s.found = b;
+        }
+        __syncthreads();
+        const int b = uniform(s.found < 0 ? s.last : s.found);
+        __syncthreads();
+        return b;
+    }
+
+    // The least key that fits (fits is false, then true), next to where it is
+    // expected: 64 keys around, one per lane, else by halves.
+    template <typename F>
+    static __device__ __forceinline__ uint32_t least_key(double guess, uint32_t top, F&& fits)
+    {
+        const float near = (float)fmin(fmax(guess, -(double)kMax), (double)kMax);
+        const uint32_t first = min(key_of(near), top) - 32;
+        const uint32_t mine = first + (threadIdx.x & 63);
+        const uint64_t yes = __ballot(mine >= top || fits(mine));
+        if ((yes & 1) == 0 && yes)
+            return uniform(first + __ffsll((long long)yes) - 1);
+        uint32_t a = key_of(-kMax), b = top;
+        while (a < b) {
+            const uint32_t mid = a + (b - a) / 2;
+            if (fits(mid))
+                b = mid;
+            else
+                a = mid + 1;
+        }
+        return uniform(a);
+    }
+    // The keys of the bins b0 .. b1.
+    __device__ __forceinline__ void keys_of(int b0, int b1, uint32_t& from, uint32_t& to) const
+    {
+        auto first = [&](int b) {  // the least key of bin b or one before
+            return least_key(scale.ref - (b + 1 - kAbove) / scale.per, key_of(kMax), [&](uint32_t key) {
+                return scale.steps(value_of(key)) < (double)(b + 1);
+            });
+        };
+        from = first(b1);
+        to = b0 ? first(b0 - 1) - 1 : key_of(kMax);
+    }
+
+    // The row's values in the bins b0 .. b1 or c0 .. c1 to cand; they fit.
+    __device__ __forceinline__ void gather(int b0, int b1, int c0, int c1)
+    {
+        uint32_t from, to, from2 = 1, to2 = 0;
+        keys_of(b0, b1, from, to);
+        if (c0 <= c1)
+            keys_of(c0, c1, from2, to2);
+        fetch(from, to, from2, to2);
+        lo[0] = b0;
+        hi[0] = b1;
+        lo[1] = c0;
+        hi[1] = c1;
+    }
+    // Values with a key in [from, to] or [from2, to2] (none where from2 > to2).
+    __device__ __forceinline__ void fetch(uint32_t from, uint32_t to, uint32_t from2, uint32_t to2)
+    {
+        constexpr int VE = Row<BF16>::VE;
+        const float x0 = value_of(from), x1 = value_of(to);
+        const float z0 = from2 <= to2 ? value_of(from2) : 1.0f, z1 = from2 <= to2 ? value_of(to2) : 0.0f;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            s.ncand = 0;
+        __syncthreads();
+        // the pass notes indices; the values follow, all at once
+        row.each([&](const float (&x)[VE], int i) {
+            uint32_t set = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                set |= (x[e] >= x0 && x[e] <= x1) || (x[e] >= z0 && x[e] <= z1) ? 1u << e : 0u;
+            if (set) {
+                uint32_t at = atomicAdd(&s.ncand, (uint32_t)__popc(set));
+                for (; set; set &= set - 1, ++at)
+                    if (at < kCap)
+                        s.cand[at] = (uint32_t)(i + __ffs(set) - 1);
+            }
+        });
+        __syncthreads();
+        const int have = min((int)s.ncand, kCap);
+        for (int i = threadIdx.x; i < have; i += kThreads) {
+            const int at = (int)s.cand[i];
+            s.cand[i] = entry(row.at(at), at);
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ bool holds(int b0, int b1) const
+    {
+        return (b0 >= lo[0] && b1 <= hi[0]) || (b0 >= lo[1] && b1 <= hi[1]);
+    }
+
+    // The values with a key in [from, to], n <= kFew of them and all in cand,
+    // sorted to the list, and the prefix sums of their weights on top of
+    // `before`.
+    __device__ __forceinline__ void collect(uint32_t from, uint32_t to, int n, double before)
+    {
+        uint32_t* rank = (uint32_t*)(s.list + 2 * kFew);
         __syncthreads();
         if (threadIdx.x == 0)
             s.n = 0;
         __syncthreads();
-        row.each([&](float x, int i) {
-            const uint32_t key = key_of(x);
-            if (key >= lo && key <= hi) {
-                const int b = scale.bin(scale.steps(x));
-                if (b >= b0 && b <= b1) {
-                    const uint32_t at = atomicAdd(&s.n, 1u);
-                    if (at < kCap)
-                        s.list[at] = ((uint64_t)~key << 32) | (uint32_t)i;
-                }
+        const int have = min((int)s.ncand, kCap);
+        for (int i = threadIdx.x; i < have; i += kThreads) {
+            const uint64_t v = s.cand[i];
+            const uint32_t key = entry_key(v);
+            if (key >= from && key <= to) {
+                const uint32_t at = atomicAdd(&s.n, 1u);
+                if (at < kFew)
+                    s.list[at] = v;
             }
-        });
+        }
+        if (threadIdx.x < kFew)
+            rank[threadIdx.x] = 0;
         __syncthreads();
-        const int n = min((int)s.n, kCap);
-        sort_list(s, n);
-        return n;
-    }
-
-    // The prefix sums of the list's weights on top of `before`.
-    __device__ void list_sums(int n, double before)
-    {
-        double w[kCap / kThreads], total = 0.0, all;
+        // four threads per value share the comparisons
+        const int i = threadIdx.x & (kFew - 1), part = threadIdx.x / kFew;
+        constexpr int EACH = kFew / (kThreads / kFew);
+        const uint64_t mine = i < n ? s.list[i] : 0;
+        if ((i & ~63) < n) {
+            uint32_t r = 0;
+            for (int j = part * EACH; j < min(n, (part + 1) * EACH); ++j)
+                r += s.list[j] < mine;
+            if (r)
+                atomicAdd(&rank[i], r);
+        }
+        __syncthreads();
+        if (part == 0 && i < n)
+            s.list[rank[i]] = mine;
+        __syncthreads();
         uint32_t c = 0, ca;
-        const int i0 = threadIdx.x * (kCap / kThreads);
-#pragma unroll
-        for (int e = 0; e < kCap / kThreads; ++e) {
-            w[e] = i0 + e < n ? scale.weight(list_key(i0 + e)) : 0.0;
-            total += w[e];
-        }
-        scan_threads(s, c, total, ca, all);
-        total += before;
-#pragma unroll
-        for (int e = 0; e < kCap / kThreads; ++e) {
-            total += w[e];
-            s.sums[i0 + e] = total;
-        }
+        const double w = part == 0 && i < n ? scale.weight(entry_key(s.list[i])) : 0.0;
+        double sum = w, all_w;
+        scan_threads(s, c, sum, ca, all_w);
+        if (part == 0)
+            s.sums[i] = before + sum + w;
         __syncthreads();
     }
 
-    // The place in the values of bin b (count and weight before it given) where
-    // `past(count, weight)`, inclusive, first holds.
+    // The place in bin b where past(count, weight), inclusive, first holds: the
+    // bin's keys are narrowed down until few values are left, or one key.
     template <typename F>
-    __device__ Place find(int b, int n, uint32_t count, double weight, bool want_index, F&& past)
+    __device__ __forceinline__ Place find(int b, F&& past)
     {
-        uint32_t lo = 0, hi = 0xFFFFFFFFu;
-        // the keys around the bin (the bin itself is checked exactly)
-        {
-            const double x1 = scale.max - b / scale.per, x0 = scale.max - (b + 1) / scale.per;
-            const double slack = 1e-6 * (fabs(x0) + fabs(x1)) + 1e-37;
-            hi = key_of((float)(x1 + slack));
-            lo = key_of((float)(x0 - slack));
-        }
+        uint32_t from, to;
+        keys_of(b, b, from, to);
+        const bool held = holds(b, b);
+        uint32_t count = s.counts[b];
+        double weight = weight_before(b);
+        int n = (int)count_in(b, b);
         Place at;
         at.index = -1;
-        // (the sums of this search go where the list is not: bins hold prefix
-        // sums that later searches use, so they are kept)
-        while (n > kCap && lo < hi) {
-            // narrow the keys down 4096 ways
-            uint64_t* sub = s.list;
-            const int shift = max(0, 32 - __clz(hi - lo) - 12);
+        at.rank = 0;
+        while (n > kFew && from < to) {
+            const int shift = max(0, 32 - __clz(to - from) - 12);
             __syncthreads();
-            for (int i = threadIdx.x; i < kBins; i += kThreads)
-                sub[i] = 0;
+            for (int i = threadIdx.x; i < kSub; i += kThreads)
+                s.list[i] = 0;
+            if (threadIdx.x == 0) {
+                s.found = kSub;
+                s.n = 0;
+            }
             __syncthreads();
-            row.each([&](float x, int) {
+            auto add = [&](float x) {
                 const uint32_t key = key_of(x);
-                if (key >= lo && key <= hi) {
-                    const double y = scale.steps(x);
-                    if (scale.bin(y) == b)
-                        atomicAdd((unsigned long long*)&sub[(hi - key) >> shift],
-                                  (unsigned long long)scale.share(y));
-                }
-            });
+                if (key >= from && key <= to)
+                    atomicAdd((unsigned long long*)&s.list[(to - key) >> shift],
+                              (unsigned long long)scale.share(scale.steps(x)));
+            };
+            if (held) {
+                const int have = min((int)s.ncand, kCap);
+                for (int i = threadIdx.x; i < have; i += kThreads)
+                    add(value_of(entry_key(s.cand[i])));
+            } else {
+                constexpr int VE = Row<BF16>::VE;
+                row.each([&](const float (&x)[VE], int) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        add(x[e]);
+                });
+            }
             __syncthreads();
             // this thread's four, and those before them
-            constexpr int PER = kBins / kThreads;
+            constexpr int PER = kSub / kThreads;
+            const double unit = scale.weight_at((double)b);
             uint32_t c = 0, ca, mine_c[PER];
             double w = 0.0, wa, mine_w[PER];
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
-                const uint64_t v = sub[threadIdx.x * PER + e];
+                const uint64_t v = s.list[threadIdx.x * PER + e];
                 mine_c[e] = scale.count(v);
-                mine_w[e] = scale.weight(v, b);
+                mine_w[e] = scale.part(v) * unit;
                 c += mine_c[e];
                 w += mine_w[e];
             }
             scan_threads(s, c, w, ca, wa);
             // the first of them where the search ends, else the last that holds any
-            if (threadIdx.x == 0) {
-                s.index = kBins;
-                s.n = 0;
-            }
-            __syncthreads();
             uint32_t before_c[PER];
             double before_w[PER];
 #pragma unroll
@@ -348,13 +684,12 @@ struct Sampler {
                 w += mine_w[e];
                 if (mine_c[e]) {
                     if (past(count + c, weight + w))
-                        atomicMin(&s.index, (int)threadIdx.x * PER + e);
+                        atomicMin(&s.found, (int)threadIdx.x * PER + e);
                     atomicMax(&s.n, (uint32_t)(threadIdx.x * PER + e));
                 }
             }
             __syncthreads();
-            const int found = s.index < kBins ? s.index : (int)s.n;
-            __syncthreads();
+            const int found = uniform(s.found < kSub ? s.found : (int)s.n);
 #pragma unroll
             for (int e = 0; e < PER; ++e)
                 if ((int)threadIdx.x * PER + e == found) {
@@ -363,30 +698,31 @@ struct Sampler {
                     s.wave_weight[0] = before_w[e];
                 }
             __syncthreads();
-            count += s.wave_count[0];
-            n = (int)s.wave_count[1];
-            weight += s.wave_weight[0];
-            const uint32_t top = hi - ((uint32_t)found << shift);
+            count = uniform(count + s.wave_count[0]);
+            n = uniform((int)s.wave_count[1]);
+            weight = uniform(weight + s.wave_weight[0]);
+            const uint32_t top = to - ((uint32_t)found << shift);
             const uint32_t span = (1u << shift) - 1;
-            lo = top - lo > span ? top - span : lo;
-            hi = top;
+            from = top - from > span ? top - span : from;
+            to = top;
             __syncthreads();
         }
-        if (n > kCap) {  // equal keys
-            at.key = lo;
-            at.weight = scale.weight(lo);
-            const int rank = 1 + first_of(n, [&](int r) {
+        if (n > kFew) {  // equal keys
+            at.key = from;
+            at.weight = scale.weight(from);
+            at.rank = 1 + first_of(n, [&](int r) {
                 return past(count + r + 1, weight + (double)(r + 1) * at.weight);
             });
-            at.upto = weight + (double)rank * at.weight;
-            if (want_index)
-                at.index = index_of(lo, rank);
+            at.upto = weight + (double)at.rank * at.weight;
             return at;
         }
-        n = gather(b, b, lo, hi);
-        list_sums(n, weight);
+        if (!held) {
+            fetch(from, to, 1, 0);
+            hi[0] = hi[1] = -1;
+        }
+        collect(from, to, n, weight);
         const int i = first_of(n, [&](int e) { return past(count + e + 1, s.sums[e]); });
-        at.key = list_key(i);
+        at.key = entry_key(s.list[i]);
         at.index = (int)(uint32_t)s.list[i];
         at.upto = s.sums[i];
         at.weight = scale.weight(at.key);
@@ -396,20 +732,24 @@ struct Sampler {
 
     // Index of the rank-th value with this key: by blocks of the row, then
     // value by value.
-    __device__ int index_of(uint32_t key, int rank)
+    __device__ __forceinline__ int index_of(uint32_t key, int rank)
     {
         uint32_t* blocks = (uint32_t*)s.list;
-        const int size = (row.V + kBins - 1) / kBins;
+        const int size = (row.V + kSub - 1) / kSub;
         __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kThreads)
+        for (int i = threadIdx.x; i < kSub; i += kThreads)
             blocks[i] = 0;
         __syncthreads();
-        row.each([&](float x, int i) {
-            if (key_of(x) == key)
-                atomicAdd(&blocks[i / size], 1u);
+        constexpr int VE = Row<BF16>::VE;
+        const int n = row.V;
+        row.each([&](const float (&x)[VE], int i) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (key_of(x[e]) == key && i + e < n)
+                    atomicAdd(&blocks[(i + e) / size], 1u);
         });
         __syncthreads();
-        constexpr int PER = kBins / kThreads;
+        constexpr int PER = kSub / kThreads;
         uint32_t c = 0, ca;
         double w = 0.0, wa;
 #pragma unroll
@@ -420,30 +760,57 @@ struct Sampler {
         for (int e = 0; e < PER; ++e) {
             const uint32_t mine = blocks[threadIdx.x * PER + e];
             if (c < (uint32_t)rank && (uint32_t)rank <= c + mine) {
-                int left = rank - (int)c;
-                for (int i = (threadIdx.x * PER + e) * size; i < row.V; ++i)
-                    if (key_of(row.at(i)) == key && --left == 0) {
-                        s.index = i;
-                        break;
-                    }
+                s.index = (threadIdx.x * PER + e) * size;
+                s.n = (uint32_t)rank - c;
             }
             c += mine;
         }
         __syncthreads();
-        const int i = s.index;
+        // every wave looks through the block, 64 values at a time
+        int i = s.index, left = (int)s.n;
+        const int lane = threadIdx.x & 63;
+        for (; ; i += 64) {
+            const bool hit = i + lane < row.V && key_of(row.at(min(i + lane, row.V - 1))) == key;
+            const uint64_t hits = __ballot(hit);
+            const int here = __popcll(hits);
+            if (left <= here || i >= row.V) {
+                const uint64_t mine = __ballot(hit && __popcll(hits & ((2ull << lane) - 1)) == left);
+                i += __ffsll((long long)mine) - 1;
+                break;
+            }
+            left -= here;
+        }
         __syncthreads();
         return i;
     }
 };
 
-template <bool BF16>
+enum Mode : int { WHOLE = 0, PART, JOIN };
+
+template <bool BF16, int MODE>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a)
 {
     __shared__ Shared s;
-    const int b = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int b = MODE == PART ? blockIdx.x / a.parts : blockIdx.x;
     const Row<BF16> row = {(const char*)a.logits + (size_t)b * a.ld * (BF16 ? 2 : 4), a.V};
+    // options that are off: k of V or more, p of 1 or more, m of 0 or less
     const float T = a.temperature ? a.temperature[b] : 1.0f;
+    const int opt_k = a.top_k ? a.top_k[b] : 0;
+    const float opt_p = a.top_p ? a.top_p[b] : 1.0f;
+    const float opt_m = a.min_p ? a.min_p[b] : 0.0f;
+    const float opt_u = MODE == PART ? 0.0f : a.u[b];
+    const double least = uniform(opt_m > 0.0f ? (double)opt_m : 0.0);
+    const int k = least > 1.0 ? 1 : (opt_k > 0 && opt_k < a.V ? opt_k : a.V);
+    const double p = uniform(opt_p < 1.0f ? fmax((double)opt_p, 0.0) : 1.0);
+    const double u = uniform(opt_u > 0.0f ? (double)opt_u : 0.0);  // (a NaN is 0)
+    const bool greedy = !(T > 0.0f);
+    const double inv_t = uniform(greedy ? 1.0 : 1.0 / (double)T);
+
+    Sampler<BF16> w = {s, row, {}, 0.0, 0, {0, 0}, {-1, -1}};
+    Scale& sc = w.scale;
+    sc.per = uniform(fmax(fmin((double)kPerUnit * inv_t, 1e300), 1e-300));
+    sc.one = uniform((double)(1ull << a.ebits));
+    sc.shift = a.ebits - 6 + (32 - __clz(a.V));
     auto finish = [&](int token, double prob) {
         if (threadIdx.x == 0) {
             a.tokens[b] = token;
@@ -452,200 +819,270 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a)
         }
     };
 
-    float m = -kInf;
-    row.each([&](float x, int) { m = fmaxf(m, x); });
+    // ---- bins and list ----
+    float ref, threshold, m;
+    Part* const parts = (Part*)a.ws + (size_t)b * a.parts;
+    if constexpr (MODE == JOIN) {
+        ref = parts[0].ref;
+        threshold = parts[0].threshold;
+        // a lane per part: maxima, and where a part's list starts
+        const int lane = threadIdx.x & 63;
+        const bool mine = lane < a.parts;
+        m = uniform(wave_max(mine ? parts[lane].max : -kInf));
+        const uint32_t n = mine ? parts[lane].n : 0;
+        const bool whole = !__any(n > kSamplePartList);
+        const uint32_t end = wave_scan(n);
+        const uint32_t all = __shfl(end, 63, 64);
+        if (whole && all <= kCap)
+            for (int q = threadIdx.x >> 6; q < a.parts; q += kWaves) {
+                const uint32_t have = __shfl(n, q, 64), at = __shfl(end, q, 64) - have;
+                for (uint32_t i = lane; i < have; i += 64)
+                    s.cand[at + i] = parts[q].list[i];
+            }
+        if (threadIdx.x == 0)
+            s.ncand = whole ? all : kCap + 1;
+        sc.ref = uniform((double)ref);
+        if (!greedy) {
+            uint64_t sum[kPer] = {};
+#pragma unroll 4
+            for (int q = 0; q < a.parts; ++q)
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        m = fmaxf(m, __shfl_xor(m, d, 64));
-    if (lane == 0)
-        s.wave_max[wave] = m;
-    __syncthreads();
+                for (int i = 1; i < kPer; ++i)
+                    sum[i] += parts[q].bins[threadIdx.x + i * kThreads];
+            // (mostly there is nothing that far above ref)
+            if (!(sc.steps(m) >= (double)kThreads))
+#pragma unroll 4
+                for (int q = 0; q < a.parts; ++q)
+                    sum[0] += parts[q].bins[threadIdx.x];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-        m = fmaxf(m, s.wave_max[w]);
+            for (int i = 0; i < kPer; ++i)
+                s.bins[threadIdx.x + i * kThreads] = sum[i];
+        }
+        __syncthreads();
+    } else {
+        w.sample(ref, threshold);
+        sc.ref = uniform((double)ref);
+        if (threadIdx.x == 0)
+            s.ncand = 0;
+        if constexpr (MODE == PART) {
+            w.clear_bins();
+            const int nv = row.vectors();
+            const int q = (int)(blockIdx.x % a.parts);
+            const int v0 = (int)((int64_t)nv * q / a.parts), v1 = (int)((int64_t)nv * (q + 1) / a.parts);
+            m = w.stream(v0, v1, q == a.parts - 1, !greedy, threshold);
+            Part& part = parts[q];
+            if (!greedy) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    part.bins[threadIdx.x + i * kThreads] = s.bins[threadIdx.x + i * kThreads];
+            }
+            const uint32_t n = s.ncand;
+            for (uint32_t i = threadIdx.x; i < n && i < kSamplePartList; i += kThreads)
+                part.list[i] = s.cand[i];
+            if (threadIdx.x == 0) {
+                part.n = n;
+                part.max = m;
+                part.ref = ref;
+                part.threshold = threshold;
+            }
+            return;
+        }
+    }
+    // the stream's maximum; a row beyond the bins goes again, from its maximum
+    // (the list is there)
+    for (bool again = MODE == JOIN; ; again = true) {
+        if (again) {
+            if (greedy || !(m < kInf) || m == -kInf || sc.steps(m) > 0.0)
+                break;
+            sc.ref = uniform((double)m);
+        }
+        w.clear_bins();
+        m = w.stream(0, row.vectors(), true, !greedy, again ? kInf : threshold);
+    }
+    const bool listed = s.ncand <= kCap;  // (the list is whole)
     if (m == -kInf) {  // nothing to choose from
         finish(-1, 0.0);
         return;
     }
-    float u = a.u[b];
-    u = u > 0.0f ? u : 0.0f;  // (a NaN is 0)
-    Sampler<BF16> sampler = {s, row, {}};
-    Scale& sc = sampler.scale;
-    if (!(T > 0.0f)) {  // the largest logit
-        finish(sampler.index_of(key_of(m), 1), 1.0);
+    // the answer: a token, or the rank-th with a key
+    uint32_t key = key_of(m);
+    int rank = 1;
+    double share = 1.0;
+    if (greedy && listed) {
+        // the largest logit: the first of the list
+        if (threadIdx.x == 0)
+            s.index = a.V;
+        __syncthreads();
+        for (int i = threadIdx.x; i < (int)s.ncand; i += kThreads)
+            if (entry_key(s.cand[i]) == key_of(m))
+                atomicMin(&s.index, (int)(uint32_t)s.cand[i]);
+        __syncthreads();
+        finish(s.index, 1.0);
         return;
     }
-    // options that are off: k of V or more, p of 1 or more, m of 0 or less
-    int k = a.top_k && a.top_k[b] > 0 && a.top_k[b] < a.V ? a.top_k[b] : a.V;
-    const double p = a.top_p && a.top_p[b] < 1.0f ? fmax((double)a.top_p[b], 0.0) : 1.0;
-    const double floor_w = a.min_p && a.min_p[b] > 0.0f ? (double)a.min_p[b] : 0.0;
-    if (floor_w > 1.0)
-        k = 1;
-    sc.max = (double)m;
-    sc.inv_t = 1.0 / (double)T;
-    sc.per = fmax(fmin((double)kPerUnit * sc.inv_t, 1e300), 1e-300);
-    sc.one = (double)(1ull << a.ebits);
-    sc.shift = a.ebits - 7 + (32 - __clz(a.V));
-    if (m == kInf) {
+    if (!greedy && m == kInf) {
         // only infinite logits have weight, all the same
+        constexpr int VE = Row<BF16>::VE;
         int n = 0;
-        row.each([&](float x, int) { n += x == kInf; });
+        row.each([&](const float (&x)[VE], int) {
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            n += __shfl_xor(n, d, 64);
+            for (int e = 0; e < VE; ++e)
+                n += x[e] == kInf;
+        });
+        uint32_t c = n, all;
+        double cw = 0.0, aw;
         __syncthreads();
-        if (lane == 0)
-            s.wave_count[wave] = n;
-        __syncthreads();
-        n = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            n += (int)s.wave_count[w];
-        n = min(n, k);
+        scan_threads(s, c, cw, all, aw);
+        n = min((int)all, k);
         if (p < 1.0)
             n = 1 + first_of(n, [&](int i) { return (double)(i + 1) >= p * n; });
-        const int r = first_of(n, [&](int i) { return (double)(i + 1) > (double)u * n; });
-        finish(sampler.index_of(key_of(m), r + 1), 1.0 / n);
-        return;
+        rank = 1 + first_of(n, [&](int i) { return (double)(i + 1) > u * n; });
+        share = 1.0 / n;
+    }
+    if (!greedy && m < kInf) {
+    sc.top = uniform(sc.steps(m));
+    w.scan_bins();
+    // every value of the bins before the threshold's is in the list
+    w.hi[0] = -1;
+    if (listed) {
+        const double y = sc.steps(threshold);
+        w.hi[0] = (y < (double)kBins ? (int)y : kBins) - 1;
     }
 
-    // ---- bins ----
-    for (int i = threadIdx.x; i < kBins; i += kThreads)
-        s.bins[i] = 0;
-    __syncthreads();
-    row.each([&](float x, int) {
-        const double y = sc.steps(x);
-        if (y < (double)kBins)
-            atomicAdd((unsigned long long*)&s.bins[(int)y], (unsigned long long)sc.share(y));
-    });
-    __syncthreads();
-    double* before = (double*)s.bins;
-    uint32_t all;
-    double total;
-    {
-        constexpr int PER = kBins / kThreads;
-        uint32_t c = 0, mine_c[PER];
-        double w = 0.0, mine_w[PER];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const uint64_t v = s.bins[threadIdx.x * PER + e];
-            mine_c[e] = sc.count(v);
-            mine_w[e] = sc.weight(v, threadIdx.x * PER + e);
-            c += mine_c[e];
-            w += mine_w[e];
-        }
-        scan_threads(s, c, w, all, total);
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            s.counts[threadIdx.x * PER + e] = c;
-            before[threadIdx.x * PER + e] = w;
-            c += mine_c[e];
-            w += mine_w[e];
-        }
-        if (threadIdx.x == 0)
-            s.counts[kBins] = all;
-        __syncthreads();
-    }
-    auto count_upto = [&](int i) { return s.counts[i + 1]; };
-    auto weight_upto = [&](int i) { return i + 1 < kBins ? before[i + 1] : total; };
-    // the last bin that holds any
-    const int last = first_of(kBins, [&](int i) { return count_upto(i) == all; });
-    auto bin_by = [&](auto&& past) {
-        return min(last, first_of(kBins, [&](int i) { return past(count_upto(i), weight_upto(i)); }));
-    };
-
-    const bool by_k = (uint32_t)k < all, by_p = p < 1.0, by_w = floor_w > 0.0 && floor_w <= 1.0;
-    // the lowest key with w >= min_p (at most the maximum's)
+    // ---- what is kept ----
+    const bool by_k = (uint32_t)k < w.all, by_p = p < 1.0, by_m = least > 0.0 && least <= 1.0;
+    // the least key with e^((x - m) / T) >= min_p
     uint32_t floor_key = 0;
-    if (by_w) {
-        uint32_t lo = key_of(-kInf), hi = key_of(m);
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (sc.weight(mid) >= floor_w)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        floor_key = lo;
-    }
-    const int bin_k = by_k ? bin_by([&](uint32_t c, double) { return c >= (uint32_t)k; }) : last;
-    int cut = bin_k;
-    if (!by_k) {
+    if (by_m)
+        floor_key = w.least_key((double)m + log(least) / inv_t, key_of(m), [&](uint32_t key) {
+            return exp(((double)value_of(key) - (double)m) * inv_t) >= least;
+        });
+    const double total = w.total;
+    int cut = s.last;
+    if (by_k) {
+        cut = w.bin_by([&](uint32_t c, double) { return c >= (uint32_t)k; });
+    } else {
         if (by_p)
-            cut = min(cut, bin_by([&](uint32_t, double w) { return w >= p * total; }));
-        if (by_w) {
-            const int f = sc.bin(sc.steps(value_of(floor_key)));
-            cut = min(cut, f < 0 ? last : f);
+            cut = w.bin_by([&](uint32_t, double x) { return x >= p * total; });
+        if (by_m) {
+            const int f = sc.bin(value_of(floor_key));
+            cut = f < 0 ? cut : min(cut, f);
         }
     }
-    if (count_upto(cut) <= kCap && (by_k || by_p || by_w || all <= kCap)) {
+    const bool cuts = by_k || by_p || by_m;
+    const int n = (int)w.count_in(0, cut);
+    if (n <= kFew && (cuts || w.holds(0, cut))) {
         // everything that matters, sorted
-        const int n = sampler.gather(0, cut, 0, 0xFFFFFFFFu);
-        sampler.list_sums(n, 0.0);
-        const double* upto = s.sums;
+        uint32_t from = 0, to = 0xFFFFFFFFu;
+        w.keys_of(0, cut, from, to);
+        if (!w.holds(0, cut))
+            w.fetch(from, to, 1, 0);
+        w.collect(from, to, n, 0.0);
         int keep = by_k ? min(n, k) : n;
-        const double of = by_k ? upto[keep - 1] : total;
+        const double of = by_k || cut == s.last ? s.sums[keep - 1] : total;
         if (by_p)
-            keep = 1 + first_of(keep, [&](int i) { return upto[i] >= p * of; });
-        if (by_w)
-            keep = max(1, first_of(keep + 1, [&](int i) { return i >= keep || sampler.list_key(i) < floor_key; }));
-        const double z = keep == n && !by_k && !by_p && !by_w ? total : upto[keep - 1];
-        const int i = first_of(keep, [&](int j) { return upto[j] > (double)u * z; });
-        finish((int)(uint32_t)s.list[i], sc.weight(sampler.list_key(i)) / z);
+            keep = 1 + first_of(keep, [&](int i) { return s.sums[i] >= p * of; });
+        if (by_m)
+            keep = max(1, first_of(keep + 1, [&](int i) { return i >= keep || entry_key(s.list[i]) < floor_key; }));
+        const double z = s.sums[keep - 1];
+        const int i = first_of(keep, [&](int j) { return s.sums[j] > u * z; });
+        finish((int)(uint32_t)s.list[i], sc.weight(entry_key(s.list[i])) / z);
         return;
     }
 
-    // one search after the other
+    // one search after the other: where top-k ends, where top-p ends, the token
     double z = total;
-    uint32_t end_key = 0;
-    Place end;
-    if (by_k) {
-        const int f = bin_k;
-        end = sampler.find(f, count_upto(f) - s.counts[f], s.counts[f], before[f], false,
-                           [&](uint32_t c, double) { return c >= (uint32_t)k; });
-        z = end.upto;
-        end_key = end.key;
+    Place at;
+    at.key = 0;
+    for (int stage = by_k ? 0 : (by_p ? 1 : 2); stage < 3; ++stage) {
+        if (stage == 1 && !by_p)
+            continue;
+        if (stage == 2 && by_m && floor_key > at.key) {
+            // the weight down to the floor's key: its bin's values above it
+            const int f0 = sc.bin(value_of(floor_key));
+            const int f = f0 < 0 ? s.last : f0;
+            constexpr int VE = Row<BF16>::VE;
+            double sum = 0.0;
+            const float least_x = value_of(floor_key);
+            row.each([&](const float (&x)[VE], int) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (x[e] >= least_x && sc.bin(x[e]) == f)
+                        sum += sc.weight(key_of(x[e]));
+            });
+            uint32_t c = 0, ca;
+            double wa;
+            scan_threads(s, c, sum, ca, wa);
+            z = uniform(fmin(z, w.weight_before(f) + wa));
+        }
+        const double target = uniform((stage == 1 ? p : u) * z);
+        auto past = [&](uint32_t c, double x) {
+            return stage == 0 ? c >= (uint32_t)k : (stage == 1 ? x >= target : x > target);
+        };
+        const int f = w.bin_by(past);
+        if (!w.holds(f, f)) {
+            // one pass: all that matters, or this bin and those that the token
+            // can lie in
+            int b0 = f, b1 = f, c0 = 1, c1 = 0;
+            if (cuts && n <= kCap) {
+                b0 = 0;
+                b1 = cut;
+            } else if (stage == 1) {
+                const double a0 = u * w.weight_before(f), a1 = u * w.weight_before(f + 1);
+                c0 = w.bin_by([&](uint32_t, double x) { return x > a0; });
+                c1 = w.bin_by([&](uint32_t, double x) { return x > a1; });
+                if ((uint64_t)w.count_in(f, f) + w.count_in(c0, c1) > kCap) {
+                    c0 = 1;
+                    c1 = 0;
+                }
+            }
+            if (w.count_in(b0, b1) <= kCap)
+                w.gather(b0, b1, c0, c1);
+        }
+        at = w.find(f, past);
+        if (stage < 2)
+            z = uniform(fmin(z, at.upto));
     }
-    if (by_p) {
-        const double target = p * z;
-        auto past = [&](uint32_t, double w) { return w >= target; };
-        const int f = bin_by(past);
-        end = sampler.find(f, count_upto(f) - s.counts[f], s.counts[f], before[f], false, past);
-        z = fmin(z, end.upto);
-        end_key = end.key;
+    share = at.weight / z;
+    if (at.rank == 0) {
+        finish(at.index, share);
+        return;
     }
-    if (by_w && floor_key > end_key) {
-        // the weight down to the floor's key: its bin's values above it
-        int f = sc.bin(sc.steps(value_of(floor_key)));
-        if (f < 0)
-            f = last;
-        double w = 0.0;
-        row.each([&](float x, int) {
-            const double y = sc.steps(x);
-            if (key_of(x) >= floor_key && sc.bin(y) == f)
-                w += exp(-(sc.max - (double)x) * sc.inv_t);
-        });
-        uint32_t c = 0, ca;
-        double wa;
-        scan_threads(s, c, w, ca, wa);
-        z = fmin(z, before[f] + wa);
+    key = at.key;
+    rank = at.rank;
     }
-    const double target = (double)u * z;
-    auto past = [&](uint32_t, double w) { return w > target; };
-    const int f = bin_by(past);
-    const Place at = sampler.find(f, count_upto(f) - s.counts[f], s.counts[f], before[f], true, past);
-    finish(at.index, at.weight / z);
+    finish(w.index_of(key, rank), share);
+}
+
+template <bool BF16>
+hipError_t launch(const SampleArgs& a, hipStream_t stream)
+{
+    if (a.parts == 1) {
+        sample_kernel<BF16, WHOLE><<<a.B, kThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    sample_kernel<BF16, PART><<<a.B * a.parts, kThreads, 0, stream>>>(a);
+    const hipError_t rc = hipGetLastError();
+    if (rc != hipSuccess)
+        return rc;
+    sample_kernel<BF16, JOIN><<<a.B, kThreads, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+int sample_parts(int64_t B, int64_t V)
+{
+    // parts of 8192 values and more, as many as fill the compute units
+    const int64_t by_values = V / 8192, by_rows = B ? 256 / B : 1;
+    const int64_t n = by_values < by_rows ? by_values : by_rows;
+    return (int)(n < 1 ? 1 : (n > 16 ? 16 : n));
+}
+int64_t sample_part_bytes() { return (int64_t)sizeof(Part); }
+
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream)
 {
-    if (a.bf16)
-        sample_kernel<true><<<a.B, kThreads, 0, stream>>>(a);
-    else
-        sample_kernel<false><<<a.B, kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    return a.bf16 ? launch<true>(a, stream) : launch<false>(a, stream);
 }
 
 }  // namespace qll

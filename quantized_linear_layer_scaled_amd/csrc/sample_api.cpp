@@ -25,7 +25,10 @@ extern "C" {
 int64_t qll_sample_workspace_bytes(int64_t B, int64_t V)
 {
     const int rc = validate(B, V);
-    return rc != QLL_OK ? -rc : 0;
+    if (rc != QLL_OK)
+        return -rc;
+    const int parts = sample_parts(B, V);
+    return parts > 1 ? B * parts * sample_part_bytes() : 0;
 }
 
 int sample_tokens(const void* logits, int logits_dtype, int64_t ld, const float* u,
@@ -47,9 +50,15 @@ int sample_tokens(const void* logits, int logits_dtype, int64_t ld, const float*
         misaligned(top_k, 4) || misaligned(top_p, 4) || misaligned(min_p, 4) ||
         misaligned(tokens, 4) || misaligned(probs, 4))
         return QLL_ERR_MISALIGNED;
-    (void)ws;
-    (void)ws_bytes;
     SampleArgs a = {};
+    a.parts = sample_parts(B, V);
+    if (a.parts > 1) {
+        if (!ws || ws_bytes < (uint64_t)(B * a.parts * sample_part_bytes()))
+            return QLL_ERR_WORKSPACE;
+        if (misaligned(ws, 16))
+            return QLL_ERR_MISALIGNED;
+        a.ws = ws;
+    }
     a.logits = logits;
     a.ld = ld;
     a.bf16 = bf16;
@@ -65,7 +74,8 @@ int sample_tokens(const void* logits, int logits_dtype, int64_t ld, const float*
     int bits = 0;
     while ((V >> bits) != 0)
         ++bits;
-    a.ebits = 71 - 2 * bits < 39 ? 71 - 2 * bits : 39;
+    // a bin's sum holds V counts above V complements below 2^(ebits - 6)
+    a.ebits = 70 - 2 * bits < 38 ? 70 - 2 * bits : 38;
     return launch_sample(a, (hipStream_t)stream) == hipSuccess ? QLL_OK : QLL_ERR_HIP;
 }
 

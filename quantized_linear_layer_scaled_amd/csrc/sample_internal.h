@@ -22,7 +22,12 @@ struct SampleArgs {
     float* probs;  // [B] or null
     int B, V;
     int ebits;  // fixed-point bits of a bin's complement (see sample.hip)
+    int parts;  // workgroups of a row
+    void* ws;   // B * parts * sample_part_bytes() where parts > 1
 };
+constexpr int kSamplePartList = 1024;
+int sample_parts(int64_t B, int64_t V);
+int64_t sample_part_bytes();
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 
 }  // namespace qll

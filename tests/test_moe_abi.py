@@ -133,6 +133,11 @@ def test_sample_refusals(L):
     for bad in (dict(x=P + 2), dict(dt=0, x=P + 1), dict(u=P + 2), dict(t=P + 1), dict(k=P + 2), dict(p=P + 2), dict(m=P + 2),
                 dict(tok=Q + 2), dict(probs=Q + 2)):
         assert sample(L, **bad) == MISALIGNED, bad
+    need = L.qll_sample_workspace_bytes(1, 151936)
+    assert need > 0 and L.qll_sample_workspace_bytes(256, 151936) == 0 == L.qll_sample_workspace_bytes(0, 9)
+    big = dict(B=1, V=151936, ld=151936)
+    assert sample(L, **big) == WORKSPACE and sample(L, **big, ws=P, wsb=need - 1) == WORKSPACE
+    assert sample(L, **big, ws=P + 8, wsb=need) == MISALIGNED
     assert sample(L, B=0, x=None, u=None, tok=None) == 0
     assert L.qll_sample_workspace_bytes(-1, 10) == -INVALID
     assert L.qll_sample_workspace_bytes(1, 1 << 21) == -UNSUPPORTED
