@@ -55,11 +55,39 @@ __device__ __forceinline__ uint8_t* ffn_alt_ring()
     return ring;
 }
 
-// Tiles first, first + step, ... of one product.
-template <bool FP8, int LAY, int EPI>
-__device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int step)
+// Where the tiles of a product lie: how many there are, the arguments and the
+// corner of tile t, and, with GATHER, the offsets in Q[0] of a tile's rows.
+// (an offset out of range stays there)
+__device__ __forceinline__ uint32_t gathered(uint32_t in_row, uint32_t row)
 {
-    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED;
+    return (in_row | row) & kOutOfRange ? kOutOfRange : in_row + row;
+}
+template <int TC>
+struct FfnDense {
+    static constexpr bool GATHER = false;
+    int tr, tc;
+    __device__ __forceinline__ explicit FfnDense(const FfnArgs& a)
+        : tr((a.R + 255) / 256), tc((a.C + TC - 1) / TC)
+    {
+    }
+    __device__ __forceinline__ int tiles() const { return tr * tc; }
+    __device__ __forceinline__ void at(int t, FfnArgs&, int& r0, int& c0) const
+    {
+        int tile_r, tile_c;
+        xcd_tile(t, tr, tc, 4, tile_r, tile_c);
+        r0 = tile_r * 256;
+        c0 = tile_c * TC;
+    }
+};
+
+// Tiles first, first + step, ... of one product.
+template <bool FP8, int LAY, int EPI, typename WHERE>
+__device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& args, const WHERE& where, int first,
+                                              int step)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_DGATED || EPI == EPI_GROUPED;
+    constexpr bool GATHER = WHERE::GATHER;
+    FfnArgs a = args;  // of the tile whose copies are being started
     using Copies = FfnCopies<FP8, LAY, DUAL, 256, 256, 4, 2>;
     using SP = typename Copies::SP;
     using SQ = typename Copies::SQ;
@@ -71,10 +99,8 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave & 3, wq = wave >> 2;  // (wq is the group)
-    constexpr int TC = DUAL ? 128 : 256;
-    const int tr = (a.R + 255) / 256, tc = (a.C + TC - 1) / TC;
     const int nk = a.nseg * a.nks;
-    const Copies cp(a, wave, lane);
+    const Copies cp(args, wave, lane);
     int c0, r0;  // corner of the tile whose copies are being started
 
     v4f acc[2][SP::NB][2][SQ::NB];
@@ -82,6 +108,7 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
     // sources of the next copies
     FfnSource<PSTR> src_p[DUAL ? 2 : 1];
     FfnSource<QSTR> src_q;
+    uint32_t row_q[GATHER ? 2 : 1][GATHER ? SQ::LD : 1];  // GATHER: the rows' offsets
     const uint32_t ldp = (uint32_t)a.ldp, ldq = (uint32_t)a.ldq;
     int kp = 0, kq = 0;
     auto set_p = [&](int seg) __attribute__((always_inline)) {
@@ -90,6 +117,23 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
             src_p[h].set(a.P[DUAL ? h : seg], ldp, c0, a.C, a.klen, FP8 ? 1 : 2, cp.vp, cp.chp);
     };
     auto set_q = [&](int seg) __attribute__((always_inline)) {
+        if constexpr (GATHER) {
+            // the offset within a row moves on with the stages, as for
+            // contiguous rows
+            where.rows(a, r0, src_q.rs);
+            src_q.v = cp.chq * 16;
+            src_q.kleft = a.klen;
+            src_q.clip(cp.chq);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < SQ::LD; ++i) {
+                    int line, ch;
+                    SQ::source(i, wave, lane, line, ch);
+                    row_q[h][i] = where.row(a, r0, ffn_tile_row<SQ, false>(h, line));
+                }
+            return;
+        }
         src_q.set(a.Q[seg], ldq, r0, a.R, a.klen, FP8 ? 1 : 2, cp.vq, cp.chq);
     };
     // (only the input gradient has a second segment)
@@ -116,8 +160,12 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
               to + (uint32_t)(slot - ring) + h * SP::HB + i * 8192);
     };
     auto copy_q = [&](int h, int i, uint8_t* slot) __attribute__((always_inline)) {
-        dma16(src_q.v + cp.shift_q(h, i), src_q.rs,
-              to + (uint32_t)(slot - ring) + 2 * SP::HB + h * SQ::HB + i * 8192);
+        uint32_t v;
+        if constexpr (GATHER)
+            v = gathered(src_q.v, row_q[h][i]);
+        else
+            v = src_q.v + cp.shift_q(h, i);
+        dma16(v, src_q.rs, to + (uint32_t)(slot - ring) + 2 * SP::HB + h * SQ::HB + i * 8192);
     };
 
     uint4 fp[2][SP::NB][2], fq[SQ::NB][2];
@@ -173,10 +221,7 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
 
     // the first two stages of tile t
     auto start = [&](int t) __attribute__((always_inline)) {
-        int tile_r, tile_c;
-        xcd_tile(t, tr, tc, 4, tile_r, tile_c);
-        r0 = tile_r * 256;
-        c0 = tile_c * TC;
+        where.at(t, a, r0, c0);
         kp = kq = 0;
         set_p(0);
         set_q(0);
@@ -195,12 +240,13 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
         }
     };
 
-    const int tiles = tr * tc;
+    const int tiles = where.tiles();
     if (first >= tiles)
         return;
     start(first);
     for (int t = first; t < tiles; t += step) {
         const int rt = r0, ct = c0;
+        const FfnArgs at = a;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -231,14 +277,15 @@ __device__ __forceinline__ void ffn_alt_tiles(const FfnArgs& a, int first, int s
         __builtin_amdgcn_sched_barrier(0);
         if (t + step < tiles)
             start(t + step);
-        ffn_finish<SP, SQ, DUAL, EPI>(a, acc, ct, rt, rt / 256, wp, wq, 2, lane);
+        ffn_finish<SP, SQ, DUAL, EPI>(at, acc, ct, rt, rt / 256, wp, wq, 2, lane);
     }
 }
 
 template <bool FP8, int LAY, int EPI>
 __global__ __launch_bounds__(512, 2) void ffn_alt_kernel(FfnArgs a)
 {
-    ffn_alt_tiles<FP8, LAY, EPI>(a, blockIdx.x, gridDim.x);
+    constexpr int TC = EPI == EPI_GATED || EPI == EPI_DGATED ? 128 : 256;
+    ffn_alt_tiles<FP8, LAY, EPI>(a, FfnDense<TC>(a), blockIdx.x, gridDim.x);
 }
 
 // Two products in one launch, the input's and the weights' gradients of a
@@ -250,12 +297,12 @@ __global__ __launch_bounds__(512, 2) void ffn_alt_pair_kernel(FfnArgs a, FfnArgs
 {
     const int tiles_a = ((a.R + 255) / 256) * ((a.C + 255) / 256);
     const int G = gridDim.x;
-    ffn_alt_tiles<false, LAY_A, EPI_PLAIN>(a, blockIdx.x, G);
+    ffn_alt_tiles<false, LAY_A, EPI_PLAIN>(a, FfnDense<256>(a), blockIdx.x, G);
     // the first tile of b whose number, after a's, is this workgroup's
     const int skip = tiles_a % G;
     const int first = (int)blockIdx.x - skip;
     __syncthreads();
-    ffn_alt_tiles<false, LAY_B, EPI_PLAIN>(b, first < 0 ? first + G : first, G);
+    ffn_alt_tiles<false, LAY_B, EPI_PLAIN>(b, FfnDense<256>(b), first < 0 ? first + G : first, G);
 }
 
 }  // namespace qll
