@@ -7,24 +7,36 @@
 //   w = scale p, or scale p / (sum of p over the chosen)
 //
 // A wave routes a token: lane l holds the VPL experts l VPL .. of it in
-// registers.  A choice is right or wrong, so values next to each other have to
-// be told apart: sums with a bias are formed in 64 bits (the vector units do
-// them at the rate of 32 bits), and without one the logits themselves are
-// compared.  The values become unsigned keys of the same order, 0 for none;
-// the k largest come out one by one, each a maximum over the wave's upper key
-// halves and, where several lanes share it, over the lower ones.
+// registers.  Values become unsigned keys of the same order, 0 for none, and
+// the k largest come out one by one, each a maximum over the wave.  Bound by
+// the vector instructions of these maxima (about 30 for 256 experts, 4 cycles
+// each), not by the logits: 8191 tokens, 256 experts, top-8, fp32: softmax 11 us,
+// 7.2 of it with top-1; sigmoid with a bias 13.5, and with 4 of 8 groups 17.
+//
+// A choice is right or wrong, so values next to each other have to be told
+// apart.  Without a bias the logits themselves are compared.  With one the sums
+// are formed in 32 bits first, with a bound on their error; where two picks, the
+// last one and the next, or the last open group and the next are closer than
+// that (one token in 400 at these sizes), the few in question, or else the
+// whole token, are formed again in 64 bits.  (All of it in 64 bits: 20 us
+// more; a wave that redoes its token takes about 3 us, and the launch waits for
+// it.)
 //
 // The sort by expert is stable and without atomics whose order would show:
 // every workgroup counts its chunk of tokens, and a second launch adds the
-// counts before its own chunk and places the choices 64 at a time, equal
+// counts before its own chunks and places the choices 64 at a time, equal
 // experts of a wave being found by comparing the bits of their numbers over
-// the lanes.  Up to kOneGroup choices a single workgroup does everything.
+// the lanes (65528 choices of 256 experts: 8.4 us).  Up to kOneGroup choices a
+// single workgroup does everything (one token, 64 experts, top-8: 5.1 us).
 #include "ffn_epilogue.h"
 #include "moe_internal.h"
 
 namespace qll {
 
 namespace {
+
+// Counts of a chunk in memory: whole 16-byte vectors.
+__host__ __device__ constexpr int hist_stride(int E) { return (E + 3) / 4 * 4; }
 
 constexpr int kOneGroup = 1024;  // choices that one workgroup sorts
 constexpr float kNan = __builtin_nanf("");
@@ -46,15 +58,15 @@ __device__ __forceinline__ T dpp_or(T none, T v)
     }
 }
 template <typename T>
-__device__ __forceinline__ T last_lane(T v)
+__device__ __forceinline__ T from_lane(T v, int lane)
 {
     if constexpr (sizeof(T) == 8) {
         const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-        const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
         return __builtin_bit_cast(T, ((uint64_t)hi << 32) | lo);
     } else {
-        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
     }
 }
 template <typename T, typename F>
@@ -66,7 +78,7 @@ __device__ __forceinline__ T wave_reduce(T v, T none, F&& f)
     v = f(v, dpp_or<0x118, 0xF>(none, v));
     v = f(v, dpp_or<0x142, 0xA>(none, v));  // row_bcast 15, 31
     v = f(v, dpp_or<0x143, 0xC>(none, v));
-    return last_lane(v);
+    return from_lane(v, 63);
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
@@ -97,31 +109,95 @@ __device__ __forceinline__ uint64_t order_key(double v)
     return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
+// e^z, the exponent's rounding and the hardware's 2^y (1 ulp) apart
+__device__ __forceinline__ float exp_f(float z)
+{
+    return __builtin_amdgcn_exp2f(z * 1.442695041f);
+}
+
+// 2^y for |y| <= 1000, to 2^-51 of itself: the Taylor series of the fraction.
+// (The library's exp and division take three times as many instructions; a
+// wave forms a value per expert.)
+__device__ __forceinline__ double pow2(double y)
+{
+    const double n = __builtin_rint(y), f = y - n;
+    double p = 2.5678435993488196e-11;
+    p = __builtin_fma(p, f, 4.44553827187081e-10);
+    p = __builtin_fma(p, f, 7.054911620801121e-09);
+    p = __builtin_fma(p, f, 1.0178086009239696e-07);
+    p = __builtin_fma(p, f, 1.3215486790144305e-06);
+    p = __builtin_fma(p, f, 1.5252733804059838e-05);
+    p = __builtin_fma(p, f, 0.00015403530393381606);
+    p = __builtin_fma(p, f, 0.0013333558146428441);
+    p = __builtin_fma(p, f, 0.009618129107628477);
+    p = __builtin_fma(p, f, 0.055504108664821576);
+    p = __builtin_fma(p, f, 0.2402265069591007);
+    p = __builtin_fma(p, f, 0.6931471805599453);
+    p = __builtin_fma(p, f, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+constexpr double kLog2e = 1.4426950408889634;
+__device__ __forceinline__ double reciprocal(double d)
+{
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    return __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+}
+
+// A lane's VPL logits of a row of E; those past the end are not numbers.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const void* p, size_t row, int E, int lane, float (&x)[VPL])
+{
+    // (all loads are under way before the first is used)
+    if constexpr (!BF16 && VPL >= 4) {
+        if (E % 4 == 0) {
+#pragma unroll
+            for (int v = 0; v < VPL; v += 4) {
+                const float4 w = *(const float4*)((const float*)p + row + min(lane * VPL + v, E - 4));
+                x[v] = w.x; x[v + 1] = w.y; x[v + 2] = w.z; x[v + 3] = w.w;
+            }
+            return;
+        }
+    }
+    if constexpr (BF16 && VPL >= 8) {
+        if (E % 8 == 0) {
+#pragma unroll
+            for (int v = 0; v < VPL; v += 8)
+                load_bf16<8>((const uint16_t*)p + row + min(lane * VPL + v, E - 8), &x[v]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        const size_t at = row + min(lane * VPL + v, E - 1);
+        x[v] = BF16 ? bf16_value(((const uint16_t*)p)[at]) : ((const float*)p)[at];
+    }
+}
+
 __device__ __forceinline__ float logit(const void* x, int bf16, size_t at)
 {
     return bf16 ? bf16_value(((const uint16_t*)x)[at]) : ((const float*)x)[at];
 }
 
-// The k largest keys, ties to the lower expert; lane j gets the j-th expert.
+// The k largest keys, ties to the lower expert; lane j gets the j-th expert,
+// and its key (0: there is none).
 template <int VPL, typename KEY>
-__device__ __forceinline__ int choose(KEY (&key)[VPL], int k, int lane)
+__device__ __forceinline__ int choose(KEY (&key)[VPL], int k, int lane, uint32_t& mine_key)
 {
     int mine = 0;
+    mine_key = 0;
     for (int j = 0; j < k; ++j) {
         KEY best = key[0];
-        int at = 0;
+        int at = lane * VPL;
 #pragma unroll
-        for (int v = 1; v < VPL; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = v;
-            }
-        uint32_t hi;
-        if constexpr (sizeof(KEY) == 8)
-            hi = (uint32_t)(best >> 32);
-        else
-            hi = best;
-        uint64_t who = __ballot(hi == wave_max(hi));
+        for (int v = 1; v < VPL; ++v) {
+            const bool more = key[v] > best;
+            best = more ? key[v] : best;
+            at = more ? lane * VPL + v : at;
+        }
+        const uint32_t hi = (uint32_t)(best >> (8 * sizeof(KEY) - 32));
+        const uint32_t most = wave_max(hi);
+        uint64_t who = __ballot(hi == most);
         if constexpr (sizeof(KEY) == 8) {
             if (who & (who - 1)) {
                 const uint32_t lo = (who >> lane) & 1 ? (uint32_t)best : 0u;
@@ -129,15 +205,28 @@ __device__ __forceinline__ int choose(KEY (&key)[VPL], int k, int lane)
             }
         }
         const int from = __ffsll((long long)who) - 1;
-        const int e = __builtin_amdgcn_readlane(lane * VPL + at, from);
-        if (lane == j)
-            mine = e;
+        const int e = __builtin_amdgcn_readlane(at, from);
+        mine = lane == j ? e : mine;
+        mine_key = lane == j ? most : mine_key;
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (lane * VPL + v == e)
-                key[v] = 0;
+            key[v] = lane * VPL + v == e ? 0 : key[v];
     }
     return mine;
+}
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+// Whether two of the first n picks, one after the other, or the last of them
+// and the next, are closer than their errors: `error`, and 2^-22 of either's
+// size.  (A lane without a pick has key 0.)
+__device__ __forceinline__ bool too_close(uint32_t key, int n, int lane, float error)
+{
+    const uint32_t after = __shfl_down(key, 1, 64);
+    const float a = key_value(key), b = key_value(after);
+    const float gap = a - b;
+    return __any(lane < n && after != 0 && gap < kInf && gap <= error + 0x1p-22f * (fabsf(a) + fabsf(b)));
 }
 
 // ---- the sort by expert ----
@@ -260,9 +349,162 @@ __device__ void sort_choices(SortShared<WAVES>& s, const SortArgs& a, ID&& id)
 
 enum Plan : int { PLAN_NONE = 0, PLAN_COUNT, PLAN_ALL };
 
+// The first n picks in the order of their sigmoids and biases in 64 bits, where
+// nothing else comes into question; `real`: a lane's pick is one.
+__device__ __forceinline__ int exact_order(const RouteArgs& a, int id, bool real, int n, int lane,
+                                           size_t row, bool bf16)
+{
+    double c = -kInf;
+    if (real) {
+        const float x = logit(a.logits, bf16, row + id);
+        const double e = pow2(fmin(fmax((double)x * -kLog2e, -1000.0), 1000.0));
+        const double p = reciprocal(1.0 + e) + (double)a.bias[id];
+        c = x == x && p == p ? p : (double)-kInf;
+    } else {
+        id = 0x7FFFFFFF;  // behind all that are
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double other = from_lane(c, i);
+        const int its = __builtin_amdgcn_readlane(id, i);
+        rank += other > c || (other == c && (its < id || (its == id && i < lane)));
+    }
+    return __builtin_amdgcn_ds_permute((lane < n ? rank : lane) << 2, id);
+}
+
+// What a lane knows of the experts: lane l holds l VPL .. of them.
+template <int VPL>
+struct Experts {
+    int E, lane;
+    int size;   // experts of a group
+    int lanes;  // lanes of a group, a power of two, or 0 where it does not fill lanes
+    float bias[VPL];
+    int group[VPL];
+
+    __device__ __forceinline__ Experts(const RouteArgs& a, int l) : E(a.sort.E), lane(l)
+    {
+        size = E / a.groups;
+        lanes = size % VPL ? 0 : size / VPL;
+        lanes = lanes & (lanes - 1) ? 0 : lanes;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int e = min(lane * VPL + v, E - 1);
+            bias[v] = a.bias ? a.bias[e] : 0.0f;
+            group[v] = min(e / size, 63);
+        }
+    }
+    __device__ __forceinline__ bool has(int v) const { return lane * VPL + v < E; }
+
+    // The open groups by the values c (`buffer`: 64 VPL of them, the wave's);
+    // margin: how far the last open one is from the next.
+    template <typename T>
+    __device__ __forceinline__ uint64_t open(const RouteArgs& a, const T (&c)[VPL], T* buffer,
+                                             T& margin) const
+    {
+        // the two largest of each group, in its first lane
+        const T none = -kInf;
+        T first = none, second = none;
+        const auto add = [&](T x) {
+            second = fmax(second, fmin(first, x));
+            first = fmax(first, x);
+        };
+        const auto join = [&](T f, T s2) {
+            second = fmax(fmax(second, s2), fmin(first, f));
+            first = fmax(first, f);
+        };
+        if (lanes) {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                add(has(v) && c[v] == c[v] ? c[v] : none);
+            // neighbours, pairs, halves and rows of 16 lanes trade theirs
+            if (lanes > 1)
+                join(dpp_or<0xB1, 0xF>(none, first), dpp_or<0xB1, 0xF>(none, second));
+            if (lanes > 2)
+                join(dpp_or<0x4E, 0xF>(none, first), dpp_or<0x4E, 0xF>(none, second));
+            if (lanes > 4)
+                join(dpp_or<0x141, 0xF>(none, first), dpp_or<0x141, 0xF>(none, second));
+            if (lanes > 8)
+                join(dpp_or<0x140, 0xF>(none, first), dpp_or<0x140, 0xF>(none, second));
+            for (int d = 16; d < lanes; d <<= 1)
+                join(__shfl_xor(first, d, 64), __shfl_xor(second, d, 64));
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                buffer[lane * VPL + v] = c[v] == c[v] ? c[v] : none;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (lane < a.groups)
+                for (int i = 0; i < size; ++i)
+                    add(buffer[lane * size + i]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        if (a.group_best > 1 && size > 1)
+            first += second;
+        // a group's rank: how many are better, or as good and before it
+        const int step = lanes ? lanes : 1;  // lanes from group to group
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const T other = from_lane(first, g * step);
+            rank += other > first || (other == first && g * step < lane);
+        }
+        const bool real = lane % step == 0 && lane < a.groups * step;
+        const uint64_t kept = __ballot(real && rank < a.keep);
+        const T last = from_lane(first, __ffsll((long long)__ballot(real && rank == a.keep - 1)) - 1);
+        const T next = from_lane(first, __ffsll((long long)__ballot(real && rank == a.keep)) - 1);
+        margin = last - next;
+        // (one bit per group)
+        uint64_t bits = 0;
+        for (uint64_t left = kept; left; left &= left - 1)
+            bits |= 1ull << ((__ffsll((long long)left) - 1) / step);
+        return bits;
+    }
+};
+
+// The choice in 64 bits: lane j gets the j-th expert.
+template <int VPL>
+__device__ __forceinline__ int exact_choice(const RouteArgs& a, const Experts<VPL>& ex,
+                                            const float (&x)[VPL], float m, double* buffer)
+{
+    double c[VPL];
+    if (a.score == SCORE_SOFTMAX) {
+        double sum = 0.0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const double e = pow2(fmax(((double)x[v] - (double)m) * kLog2e, -1000.0));
+            c[v] = x[v] > -kInf ? e : 0.0;
+            sum += c[v];
+        }
+        sum = wave_sum(sum);
+        const double scale = sum > 0.0 ? reciprocal(sum) : 0.0;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            c[v] = x[v] == x[v] ? c[v] * scale : kNan;
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const double e = pow2(fmin(fmax((double)x[v] * -kLog2e, -1000.0), 1000.0));
+            const double p = reciprocal(1.0 + e);
+            c[v] = x[v] == x[v] ? p : kNan;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+        c[v] += (double)ex.bias[v];
+    uint32_t unused;
+    double margin;
+    const uint64_t open = a.keep < a.groups ? ex.open(a, c, buffer, margin) : ~0ull;
+    uint64_t key[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        // without a bias the logits decide
+        const uint64_t k = a.bias ? order_key(c[v]) : (uint64_t)order_key(x[v]) << 32;
+        key[v] = ex.has(v) && ((open >> ex.group[v]) & 1) ? k : 0;
+    }
+    return choose(key, a.sort.k, ex.lane, unused);
+}
+
 // Tokens blockIdx.x * chunk ..; PLAN_COUNT: and the chunk's counts; PLAN_ALL:
 // one workgroup, all tokens, and the sort.
-template <int VPL, int WAVES, int PLAN>
+template <int VPL, bool BF16, int WAVES, int PLAN>
 __global__ __launch_bounds__(WAVES * 64) void moe_route_kernel(RouteArgs a)
 {
     const SortArgs& s = a.sort;
@@ -273,114 +515,108 @@ __global__ __launch_bounds__(WAVES * 64) void moe_route_kernel(RouteArgs a)
     __shared__ int counts[PLAN == PLAN_COUNT ? 64 * VPL : 1];
     __shared__ int chosen[PLAN == PLAN_ALL ? kOneGroup : 1];
     if constexpr (PLAN == PLAN_COUNT) {
-        for (int e = threadIdx.x; e < E; e += WAVES * 64)
+        for (int e = threadIdx.x; e < hist_stride(E); e += WAVES * 64)
             counts[e] = 0;
         __syncthreads();
     }
     const bool grouped = a.keep < a.groups;
-    const int size = E / a.groups;
-    float bias[VPL];
-    int group[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const int e = lane * VPL + v;
-        bias[v] = a.bias && e < E ? a.bias[e] : 0.0f;
-        group[v] = min(e / size, 63);
-    }
+    const Experts<VPL> ex(a, lane);
 
     const int t0 = blockIdx.x * s.chunk, t1 = min(s.T, t0 + s.chunk);
+    float next[VPL];
+    if (t0 + wave < t1)
+        load_logits<VPL, BF16>(a.logits, (size_t)(t0 + wave) * E, E, lane, next);
     for (int t = t0 + wave; t < t1; t += WAVES) {
-        const size_t row = (size_t)t * E;
         float x[VPL];
         float m = -kInf;
         bool bad = false;  // a row whose softmax is not a number
 #pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            x[v] = lane * VPL + v < E ? next[v] : -kInf;
+        if (t + WAVES < t1)  // (the next token's are on their way under this one)
+            load_logits<VPL, BF16>(a.logits, (size_t)(t + WAVES) * E, E, lane, next);
+#pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const int e = lane * VPL + v;
-            x[v] = e < E ? logit(a.logits, a.bf16, row + e) : -kInf;
             m = fmaxf(m, x[v]);
             bad |= !(x[v] < kInf);
         }
+        bad = __any(bad);
         float z = 0.0f;
+        // scores, and what two of them may be off by (a sigmoid 1.1 2^-22)
+        float c[VPL];
+        float error = 0x1p-20f;
         if (a.score == SCORE_SOFTMAX) {
             m = wave_max(m);
-            bad = __any(bad);
-            if (!a.renorm) {
+            if (!a.renorm || grouped || a.bias) {
 #pragma unroll
-                for (int v = 0; v < VPL; ++v)
-                    z += m > -kInf ? expf(x[v] - m) : 0.0f;
+                for (int v = 0; v < VPL; ++v) {
+                    c[v] = m > -kInf ? exp_f(x[v] - m) : 0.0f;
+                    z += c[v];
+                }
                 z = wave_sum(z);
             }
         }
-        double c[VPL];  // what groups, and choices with a bias, go by
+        int id = 0;
+        float l = 0.0f;  // lane j: the j-th expert and its logit
+        uint32_t picked;
+        bool again = false;  // too close to call
+        uint64_t open = ~0ull;  // groups to choose from
         if (grouped || a.bias) {
             if (a.score == SCORE_SOFTMAX) {
-                double sum = 0.0;
-#pragma unroll
-                for (int v = 0; v < VPL; ++v) {
-                    c[v] = m > -kInf ? exp((double)x[v] - (double)m) : 0.0;
-                    sum += c[v];
-                }
-                sum = wave_sum(sum);
+                // (p D < 0.4 for p = e^-D; the sum's error adds 40 u of p <= 1 / z)
+                const float iz = z > 0.0f ? 1.0f / z : 0.0f;
+                error = 0x1p-22f * (0.5f + 42.0f * iz);
 #pragma unroll
                 for (int v = 0; v < VPL; ++v)
-                    c[v] = sum > 0.0 ? c[v] / sum : c[v];
+                    c[v] *= iz;
             } else {
 #pragma unroll
                 for (int v = 0; v < VPL; ++v)
-                    c[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+                    c[v] = sigmoid_f(x[v]);
             }
 #pragma unroll
             for (int v = 0; v < VPL; ++v)
-                c[v] += (double)bias[v];
-        }
-        uint64_t open = ~0ull;  // groups to choose from
-        if (grouped) {
-            double* mine = group_value[wave];
+                c[v] += ex.bias[v];
+            if (grouped) {
+                // (the sums' roundings, of four values and two sums)
+                float most = 0.0f;
 #pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                mine[lane * VPL + v] = c[v] == c[v] ? c[v] : (double)-kInf;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            double first = -kInf, second = -kInf;
-            if (lane < a.groups)
-                for (int i = 0; i < size; ++i) {
-                    const double v = mine[lane * size + i];
-                    second = fmax(second, fmin(first, v));
-                    first = fmax(first, v);
-                }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (a.group_best > 1 && size > 1)
-                first += second;
-            uint64_t key[1] = {lane < a.groups ? order_key(first) : 0};
-            const int g = choose<1>(key, a.keep, lane);
-            open = 0;
-            for (int j = 0; j < a.keep; ++j)
-                open |= 1ull << __builtin_amdgcn_readlane(g, j);
+                for (int v = 0; v < VPL; ++v)
+                    most = fmaxf(most, fabsf(c[v]));
+                const float group_error = 0x1p-20f * wave_max(most);
+                float margin;
+                open = ex.open(a, c, (float*)group_value[wave], margin);
+                again = !(margin > 2.0f * error + group_error);
+            }
         }
-        auto pickable = [&](int v) {
-            return lane * VPL + v < E && ((open >> group[v]) & 1);
-        };
-        int id;
-        if (a.bias) {
-            uint64_t key[VPL];
+        uint32_t key[VPL];
 #pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                key[v] = pickable(v) ? order_key(c[v]) : 0;
-            id = choose(key, k, lane);
-        } else {
-            uint32_t key[VPL];
-#pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                key[v] = pickable(v) ? order_key(x[v]) : 0;
-            id = choose(key, k, lane);
-        }
-        float w = 0.0f;
-        if (lane < k) {
-            const float l = logit(a.logits, a.bf16, row + id);
-            if (a.score == SCORE_SIGMOID)
-                w = 1.0f / (1.0f + expf(-l));
+        for (int v = 0; v < VPL; ++v)
+            key[v] = ex.has(v) && ((open >> ex.group[v]) & 1) ? order_key(a.bias ? c[v] : x[v]) : 0;
+        id = choose(key, a.bias ? k + 2 : k, lane, picked);
+        if (a.bias && too_close(picked, k, lane, error)) {
+            // sigmoids: the picks and the next two in 64 bits, if no others come
+            // into question
+            const uint32_t after = k + 1 < 64 ? (uint32_t)__builtin_amdgcn_readlane((int)picked, k + 1) : 1u;
+            const float last = key_value(__builtin_amdgcn_readlane((int)picked, k - 1)), next = key_value(after);
+            const bool enough = after == 0 || last - next > error + 0x1p-22f * (fabsf(last) + fabsf(next));
+            if (a.score == SCORE_SIGMOID && !again && enough && k + 2 <= 64)
+                id = exact_order(a, id, picked != 0, k + 2, lane, (size_t)t * E, BF16);
             else
-                w = bad ? kNan : (m > -kInf ? expf(l - m) : 0.0f);
+                again = true;
+        }
+        if (again)
+            id = exact_choice(a, ex, x, m, group_value[wave]);
+        if (lane < k)
+            l = again || a.bias || bad ? logit(a.logits, BF16, (size_t)t * E + id) : key_value(picked);
+        float w = 0.0f;
+        if (a.score == SCORE_SOFTMAX && a.renorm)
+            m = wave_max(lane < k ? l : -kInf);
+        if (lane < k) {
+            if (a.score == SCORE_SIGMOID)
+                w = sigmoid_f(l);
+            else
+                w = bad ? kNan : (m > -kInf ? exp_f(l - m) : 0.0f);
         }
         if (a.renorm)
             z = wave_sum(w);
@@ -397,8 +633,8 @@ __global__ __launch_bounds__(WAVES * 64) void moe_route_kernel(RouteArgs a)
     }
     if constexpr (PLAN == PLAN_COUNT) {
         __syncthreads();
-        for (int e = threadIdx.x; e < E; e += WAVES * 64)
-            s.hist[(size_t)blockIdx.x * E + e] = counts[e];
+        for (int e = threadIdx.x; e < hist_stride(E); e += WAVES * 64)
+            s.hist[(size_t)blockIdx.x * hist_stride(E) + e] = counts[e];
     }
     if constexpr (PLAN == PLAN_ALL) {
         __shared__ SortShared<WAVES> shared;
@@ -417,7 +653,7 @@ __global__ __launch_bounds__(1024) void moe_sort_kernel(SortArgs a)
 __global__ __launch_bounds__(256) void moe_count_kernel(SortArgs a)
 {
     __shared__ int counts[kMoeMaxExperts];
-    for (int e = threadIdx.x; e < a.E; e += 256)
+    for (int e = threadIdx.x; e < hist_stride(a.E); e += 256)
         counts[e] = 0;
     __syncthreads();
     const int i0 = blockIdx.x * a.chunk * a.k;
@@ -428,37 +664,44 @@ __global__ __launch_bounds__(256) void moe_count_kernel(SortArgs a)
             atomicAdd(&counts[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 256)
-        a.hist[(size_t)blockIdx.x * a.E + e] = counts[e];
+    for (int e = threadIdx.x; e < hist_stride(a.E); e += 256)
+        a.hist[(size_t)blockIdx.x * hist_stride(a.E) + e] = counts[e];
 }
 
 // Places the choices of `per` chunks.
-__global__ __launch_bounds__(512) void moe_place_kernel(SortArgs a)
+__global__ __launch_bounds__(1024) void moe_place_kernel(SortArgs a)
 {
-    __shared__ SortShared<8> s;
+    constexpr int N = 1024;
+    __shared__ SortShared<N / 64> s;
     const int c0 = blockIdx.x * a.per, c1 = min(a.chunks, c0 + a.per);
-    for (int e = threadIdx.x; e < a.E; e += 512)
+    for (int e = threadIdx.x; e < a.E; e += N)
         s.base[e] = s.total[e] = 0;
     __syncthreads();
     // the counts of all chunks, and of those before c0: the threads share the
-    // chunks of an expert
-    const int parts = max(512 / a.E, 1);
-    for (int x = threadIdx.x; x < parts * a.E; x += 512) {
-        const int e = x % a.E, p = x / a.E;
-        int sum = 0, before = 0;
+    // chunks of four experts
+    const int fours = hist_stride(a.E) / 4, parts = N / fours;
+    const int f = threadIdx.x % fours, p = threadIdx.x / fours;
+    if (p < parts) {
+        int4 sum = {0, 0, 0, 0}, before = {0, 0, 0, 0};
 #pragma unroll 8
         for (int c = p; c < a.chunks; c += parts) {
-            const int n = a.hist[(size_t)c * a.E + e];
-            sum += n;
-            before += c < c0 ? n : 0;
+            const int4 n = *(const int4*)(a.hist + (size_t)c * (4 * fours) + 4 * f);
+            const int in = c < c0 ? -1 : 0;
+            sum.x += n.x; sum.y += n.y; sum.z += n.z; sum.w += n.w;
+            before.x += n.x & in; before.y += n.y & in; before.z += n.z & in; before.w += n.w & in;
         }
-        atomicAdd(&s.total[e], sum);
-        atomicAdd(&s.base[e], before);
+        const int all[4] = {sum.x, sum.y, sum.z, sum.w}, less[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * f + i < a.E) {
+                atomicAdd(&s.total[4 * f + i], all[i]);
+                atomicAdd(&s.base[4 * f + i], less[i]);
+            }
     }
     __syncthreads();
     const int placed = scan_experts(s, a.E, a.offsets, blockIdx.x == 0);
     const int n = a.T * a.k;
-    for (int i = placed + blockIdx.x * 512 + (int)threadIdx.x; i < n; i += gridDim.x * 512)
+    for (int i = placed + blockIdx.x * N + (int)threadIdx.x; i < n; i += gridDim.x * N)
         a.rows[i] = -1;
     place_choices(s, a, c0 * a.chunk * a.k, min(a.T, c1 * a.chunk) * a.k,
                   [&](int i) { return a.ids[i]; });
@@ -468,7 +711,7 @@ __global__ __launch_bounds__(512) void moe_place_kernel(SortArgs a)
 //   softmax      dx = p (dp - <dp, p>), dp = scale dw at the chosen
 //   renormalised the same over the chosen alone
 //   sigmoid      dx = dp p (1 - p), renormalised dp = (dw - <dw, r>) / sum p
-template <int VPL>
+template <int VPL, bool BF16>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardArgs a)
 {
     const int lane = threadIdx.x & 63;
@@ -476,20 +719,22 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardAr
     if (t >= a.T)
         return;
     const size_t row = (size_t)t * a.E;
+    const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
+    float all[VPL];
+    if (dense)
+        load_logits<VPL, BF16>(a.logits, row, a.E, lane, all);
     const int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
     const bool live = (unsigned)id < (unsigned)a.E;
     const float dw = live ? a.scale * a.dweights[(size_t)t * a.k + lane] : 0.0f;
-    const float xc = live ? logit(a.logits, a.bf16, row + id) : -kInf;
+    const float xc = live ? logit(a.logits, BF16, row + id) : -kInf;
     float g;      // the gradient that reaches logit `id`
     float x[VPL], p[VPL];
     float dot = 0.0f;
-    const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
     if (dense) {
         float m = -kInf, z = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const int e = lane * VPL + v;
-            x[v] = e < a.E ? logit(a.logits, a.bf16, row + e) : -kInf;
+            x[v] = lane * VPL + v < a.E ? all[v] : -kInf;
             m = fmaxf(m, x[v]);
         }
         m = wave_max(m);
@@ -539,7 +784,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardAr
     for (int v = 0; v < VPL; ++v) {
         const int e = lane * VPL + v;
         if (e < a.E) {
-            if (a.bf16)
+            if constexpr (BF16)
                 ((uint16_t*)a.dlogits)[row + e] = bf16_one(d[v]);
             else
                 ((float*)a.dlogits)[row + e] = d[v];
@@ -547,19 +792,25 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardAr
     }
 }
 
-// f(integral_constant<experts per lane>)
-template <typename F>
+// f(integral_constant<experts per lane>, integral_constant<bf16>)
+template <bool BF16, typename F>
 hipError_t with_vpl(int E, F&& f)
 {
+    constexpr std::integral_constant<bool, BF16> type = {};
     if (E <= 64)
-        return f(std::integral_constant<int, 1>{});
+        return f(std::integral_constant<int, 1>{}, type);
     if (E <= 128)
-        return f(std::integral_constant<int, 2>{});
+        return f(std::integral_constant<int, 2>{}, type);
     if (E <= 256)
-        return f(std::integral_constant<int, 4>{});
+        return f(std::integral_constant<int, 4>{}, type);
     if (E <= 512)
-        return f(std::integral_constant<int, 8>{});
-    return f(std::integral_constant<int, 16>{});
+        return f(std::integral_constant<int, 8>{}, type);
+    return f(std::integral_constant<int, 16>{}, type);
+}
+template <typename F>
+hipError_t with_logits(int E, int bf16, F&& f)
+{
+    return bf16 ? with_vpl<true>(E, f) : with_vpl<false>(E, f);
 }
 
 }  // namespace
@@ -572,37 +823,40 @@ int64_t moe_sort_plan(SortArgs& a)
         a.chunks = a.per = 1;
         return 0;
     }
-    // at most 512 chunks, and 256 workgroups that place about 1024 choices or
-    // more each
+    // Chunks of 16 tokens (one for each wave) up to 4096, then of 32; at most
+    // 512 of them, and at most 256 workgroups that place whole batches of 1024
+    // choices or, of large chunks, one each.
     const int64_t chunk = ((int64_t)a.T + 511) / 512;
-    a.chunk = (int)(chunk < 32 ? 32 : (chunk + 31) / 32 * 32);
+    a.chunk = a.T <= 4096 ? 16 : (int)(chunk < 32 ? 32 : (chunk + 31) / 32 * 32);
     a.chunks = (a.T + a.chunk - 1) / a.chunk;
-    const int64_t want = n / 1024 < 1 ? 1 : (n / 1024 > 256 ? 256 : n / 1024);
-    a.per = (int)((a.chunks + want - 1) / want);
-    return (int64_t)a.chunks * a.E * 4;
+    const int batch = 1024 / (a.chunk * a.k), least = (a.chunks + 255) / 256;
+    a.per = batch > least ? batch : least;
+    return (int64_t)a.chunks * hist_stride(a.E) * 4;
 }
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream)
 {
     const SortArgs& s = a.sort;
-    hipError_t rc = with_vpl(s.E, [&](auto V) {
+    hipError_t rc = with_logits(s.E, a.bf16, [&](auto V, auto B) {
         constexpr int VPL = decltype(V)::value;
+        constexpr bool BF16 = decltype(B)::value;
         if (!s.offsets) {
             RouteArgs b = a;
             b.sort.chunk = 4;
-            moe_route_kernel<VPL, 4, PLAN_NONE><<<(s.T + 3) / 4, 256, 0, stream>>>(b);
+            moe_route_kernel<VPL, BF16, 4, PLAN_NONE><<<(s.T + 3) / 4, 256, 0, stream>>>(b);
         } else if (!s.hist) {
             // (the groups' values of 16 waves would not fit in LDS)
             constexpr int WAVES = VPL >= 16 ? 8 : 16;
-            moe_route_kernel<VPL, WAVES, PLAN_ALL><<<1, WAVES * 64, 0, stream>>>(a);
+            moe_route_kernel<VPL, BF16, WAVES, PLAN_ALL><<<1, WAVES * 64, 0, stream>>>(a);
         } else {
-            moe_route_kernel<VPL, 8, PLAN_COUNT><<<s.chunks, 512, 0, stream>>>(a);
+            constexpr int WAVES = VPL >= 16 ? 8 : 16;
+            moe_route_kernel<VPL, BF16, WAVES, PLAN_COUNT><<<s.chunks, WAVES * 64, 0, stream>>>(a);
         }
         return hipGetLastError();
     });
     if (rc != hipSuccess || !s.hist)
         return rc;
-    moe_place_kernel<<<(s.chunks + s.per - 1) / s.per, 512, 0, stream>>>(s);
+    moe_place_kernel<<<(s.chunks + s.per - 1) / s.per, 1024, 0, stream>>>(s);
     return hipGetLastError();
 }
 
@@ -616,14 +870,14 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t stream)
     const hipError_t rc = hipGetLastError();
     if (rc != hipSuccess)
         return rc;
-    moe_place_kernel<<<(a.chunks + a.per - 1) / a.per, 512, 0, stream>>>(a);
+    moe_place_kernel<<<(a.chunks + a.per - 1) / a.per, 1024, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_moe_route_backward(const RouteBackwardArgs& a, hipStream_t stream)
 {
-    return with_vpl(a.E, [&](auto V) {
-        moe_route_backward_kernel<decltype(V)::value><<<(a.T + 3) / 4, 256, 0, stream>>>(a);
+    return with_logits(a.E, a.bf16, [&](auto V, auto B) {
+        moe_route_backward_kernel<decltype(V)::value, decltype(B)::value><<<(a.T + 3) / 4, 256, 0, stream>>>(a);
         return hipGetLastError();
     });
 }
