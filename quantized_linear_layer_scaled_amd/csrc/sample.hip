@@ -538,30 +538,30 @@ struct Sampler {
     {
         constexpr int VE = Row<BF16>::VE;
         const float x0 = value_of(from), x1 = value_of(to);
-        const float z0 = from2 <= to2 ? value_of(from2) : 1.0f, z1 = from2 <= to2 ? value_of(to2) : 0.0f;
+        const bool two = from2 <= to2;
+        const float z0 = two ? value_of(from2) : 1.0f, z1 = two ? value_of(to2) : 0.0f;
         __syncthreads();
         if (threadIdx.x == 0)
             s.ncand = 0;
         __syncthreads();
-        // the pass notes indices; the values follow, all at once
         row.each([&](const float (&x)[VE], int i) {
-            uint32_t set = 0;
+            // at least 0 if a value may lie between (comparisons would need
+            // scalar instructions for each)
+            float near = -1.0f;
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                set |= (x[e] >= x0 && x[e] <= x1) || (x[e] >= z0 && x[e] <= z1) ? 1u << e : 0u;
-            if (set) {
-                uint32_t at = atomicAdd(&s.ncand, (uint32_t)__popc(set));
-                for (; set; set &= set - 1, ++at)
-                    if (at < kCap)
-                        s.cand[at] = (uint32_t)(i + __ffs(set) - 1);
+                near = fmaxf(near, fminf(x[e] - x0, x1 - x[e]));
+            if (two)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    near = fmaxf(near, fminf(x[e] - z0, z1 - x[e]));
+            if (near >= 0.0f) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if ((x[e] >= x0 && x[e] <= x1) || (x[e] >= z0 && x[e] <= z1))
+                        keep(x[e], i + e);
             }
         });
-        __syncthreads();
-        const int have = min((int)s.ncand, kCap);
-        for (int i = threadIdx.x; i < have; i += kThreads) {
-            const int at = (int)s.cand[i];
-            s.cand[i] = entry(row.at(at), at);
-        }
         __syncthreads();
     }
     __device__ __forceinline__ bool holds(int b0, int b1) const
