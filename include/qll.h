@@ -504,7 +504,7 @@ int64_t qll_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t topk);
  *   expert owns are left unwritten); rows int32 [R]: a token outside [0, T)
  *   reads as zeros; out bf16 / fp32 [R][N].  K % 16 == 0, any N, E <= 65536.
  *   With rows, T * K < 2^31 (UNSUPPORTED beyond, as are outputs of more tiles
- *   than a launch holds, about R N = 2^35).  R == 0 is a no-op. */
+ *   than a launch holds, R N of about 2^35).  R == 0 is a no-op. */
 int gated_fp8_grouped(const void* A, const void* Bg, const void* Bu, const float* sa,
                       const float* sg, const float* su, const int32_t* offsets,
                       const int32_t* rows, int act, void* out, int out_dtype, int64_t T, int64_t R,
@@ -523,7 +523,7 @@ int moe_combine(const void* y, const int32_t* places, const float* weights, cons
 /* Its backward pass (the residual's gradient is dout itself):
  *   dy[places[t][j]] = weights[t][j] dout[t],  dweights[t][j] = <dout[t], y[places[t][j]]>
  *   dout bf16 / fp32 [T][K] (dout_dtype); dy bf16 [R][K] or NULL: rows that no
- *   place names are left unwritten, and one that two places name holds either's;
+ *   place names are left unwritten, one that two places name holds values of either;
  *   dweights fp32 [T][topk] or NULL (needs y, else NULL; 0 without a row). */
 int moe_combine_backward(const void* y, const int32_t* places, const float* weights,
                          const void* dout, int dout_dtype, void* dy, float* dweights, int64_t T,
@@ -545,7 +545,8 @@ int moe_combine_backward(const void* y, const int32_t* places, const float* weig
  * A temperature of 0, below or NaN takes the first token (probs 1).  NaN and
  * -infinity are never chosen: a row of nothing else gives token -1, probs 0.
  * A row with +infinity gives all of these the weight 1, the others none.
- * Weights are formed in 64 bits; those below e^-32 are taken as 0.
+ * Weights are formed in 64 bits; below e^-31.9 of the largest they may be
+ * taken as 0.
  *   logits bf16 or fp32 [B] rows of V values, `ld` values apart (ld >= V), of
  *   their type's alignment; u fp32 [B] in [0, 1); temperature, top_p, min_p
  *   fp32 [B], top_k int32 [B], each NULL for 1 or off; tokens int32 [B]; probs

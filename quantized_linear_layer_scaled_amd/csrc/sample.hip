@@ -22,8 +22,8 @@
 // with f the fraction of the bin (64-bit arithmetic, four terms: 2^-37), and
 // the additions are integers: the count above, g in `ebits` fractional bits
 // below (34 for vocabularies below 2^18), which no order of additions changes.
-// Weights below e^-32 of the largest are left out: 2^20 of them are less than
-// 1.4e-8 of the total, below the last bit of u next to 1 (6e-8).
+// Weights below e^-31.9 of the largest are left out: 2^20 of them are less than
+// 1.5e-8 of the total, below the last bit of u next to 1 (6e-8).
 //
 // The bins cover 16 T above ref and 32 T below; a row whose maximum lies above
 // starts again with ref = the maximum.  A bin that holds more values than the
@@ -41,9 +41,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 3072;
+constexpr int kPer = 3;                  // bins of a thread
+constexpr int kBins = kPer * kThreads;
 constexpr int kPerUnit = 64;             // bins per unit of (ref - x) / T
-constexpr int kPer = kBins / kThreads;   // bins of a thread
 // the bin of ref, 16 units above (a thread's first, whose weight at ref is
 // exactly 1: equal weights stay equal)
 constexpr int kAbove = 16 * kPerUnit / kPer * kPer + kPer;
