@@ -28,7 +28,7 @@ __device__ __forceinline__ void load8(const void* p, size_t at, float* f)
 // A thread per 8 columns of a token; the rows of FOUR choices are under way at a
 // time.  ALIGNED: topk is a multiple of four, so places and weights come as
 // vectors.  (One choice at a time, each behind its place: T = 4093, top-8,
-// K = 4104 70 us; this way 66, 5.1 TB/s.)
+// K = 4104 70 us; this way 65, 5.2 TB/s.)
 template <bool F32, bool ALIGNED>
 __global__ __launch_bounds__(256) void moe_combine_kernel(CombineArgs a)
 {
