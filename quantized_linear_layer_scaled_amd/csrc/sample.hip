@@ -203,7 +203,7 @@ struct Row {
 // The order of a row's weights.
 struct Scale {
     double ref, per;  // bins: (ref - x) per + kAbove
-    double one;       // 2^ebits
+    double one, unit;  // 2^ebits, 2^-ebits
     double top;       // steps(maximum): the place of weight 1
     int shift;        // of the count
 
@@ -238,7 +238,7 @@ struct Scale {
     // a bin's weight over that of its upper end
     __device__ __forceinline__ double part(uint64_t sum) const
     {
-        return (double)count(sum) - (double)(sum & ((1ull << shift) - 1)) / one;
+        return (double)count(sum) - (double)(sum & ((1ull << shift) - 1)) * unit;
     }
     __device__ __forceinline__ double weight_at(double y) const
     {
@@ -476,24 +476,22 @@ struct Sampler {
     }
 
     // The first bin up to which past(count, weight) holds, else the last that
-    // holds values.
+    // holds values: every wave by itself, 64 bins a look, and no barrier.
     template <typename F>
-    __device__ __forceinline__ int bin_by(F&& past)
+    __device__ __forceinline__ int bin_by(F&& past) const
     {
-        if (threadIdx.x == 0)
-            s.found = -1;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int b = threadIdx.x * kPer + i;
-            const uint32_t c0 = s.counts[b], c1 = s.counts[b + 1];
-            if (c1 > c0 && past(c1, weight_before(b + 1)) && (c0 == 0 || !past(c0, weight_before(b))))
-                s.found = b;
-        }
-        __syncthreads();
-        const int b = uniform(s.found < 0 ? s.last : s.found);
-        __syncthreads();
-        return b;
+        constexpr int EACH = kBins / 64;
+        static_assert(EACH <= 64);
+        const int lane = threadIdx.x & 63;
+        auto look = [&](int b) {  // first lane whose bin is past it, 64 for none
+            const uint32_t c = s.counts[b + 1];
+            const uint64_t yes = __ballot(c > 0 && past(c, weight_before(b + 1)));
+            return yes ? __ffsll((long long)yes) - 1 : 64;
+        };
+        const int run = look(lane * EACH + EACH - 1);
+        if (run == 64)
+            return uniform(s.last);
+        return uniform(run * EACH + look(run * EACH + min(lane, EACH - 1)));
     }
 
     // The least key that fits (fits is false, then true), next to where it is
@@ -819,6 +817,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a)
     Scale& sc = w.scale;
     sc.per = uniform(fmax(fmin((double)kPerUnit * inv_t, 1e300), 1e-300));
     sc.one = uniform((double)(1ull << a.ebits));
+    sc.unit = 1.0 / sc.one;
     sc.shift = a.ebits - 6 + (32 - __clz(a.V));
     auto finish = [&](int token, double prob) {
         if (threadIdx.x == 0) {
