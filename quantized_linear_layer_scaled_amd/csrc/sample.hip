@@ -552,20 +552,24 @@ struct Sampler {
             s.ncand = 0;
         __syncthreads();
         row.each([&](const float (&x)[VE], int i) {
-            // at least 0 if a value may lie between (comparisons would need
-            // scalar instructions for each)
-            float near = -1.0f;
+            // at least 0 where a value lies between (comparisons would need
+            // scalar instructions for each; differences have the right sign)
+            float in[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e)
-                near = fmaxf(near, fminf(x[e] - x0, x1 - x[e]));
+                in[e] = fminf(x[e] - x0, x1 - x[e]);
             if (two)
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    near = fmaxf(near, fminf(x[e] - z0, z1 - x[e]));
-            if (near >= 0.0f) {
+                    in[e] = fmaxf(in[e], fminf(x[e] - z0, z1 - x[e]));
+            float any = in[0];
+#pragma unroll
+            for (int e = 1; e < VE; ++e)
+                any = fmaxf(any, in[e]);
+            if (any >= 0.0f) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if ((x[e] >= x0 && x[e] <= x1) || (x[e] >= z0 && x[e] <= z1))
+                    if (in[e] >= 0.0f)
                         keep(x[e], i + e);
             }
         });
