@@ -33,14 +33,14 @@
 // A workgroup takes a row, or one of `parts` of it where there are few rows;
 // then a second launch adds the parts' bins and finishes.
 //
-// Measured: one row of 151936 bf16 logits in 16 parts 7.9 us, the second launch
-// 16 where the list holds the answer and up to 53 for a flat row under top-p;
-// 256 fp32 rows of mixed options 101: 33 for the read (4.7 TB/s), then the
-// flattest row's second read 37 and its two searches 22; 48 rows of 50021 under
-// top-p 10 and 42.  Past the first read a row is a chain of short steps of one
+// Measured: one row of 151936 bf16 logits in 16 parts 7.5 us, the second launch
+// 16 where the list holds the answer and up to 47 for a flat row under top-p;
+// 256 fp32 rows of mixed options 93: 33 for the read (4.7 TB/s), then the
+// flattest row's second read 30 and its two searches 22; 48 rows of 50021 under
+// top-p 10 and 37.  Past the first read a row is a chain of short steps of one
 // workgroup.  (The second read over as many workgroups as the first: 26 us in
 // place of 36 for one row, but 29 in place of 21 for 48, the joining of the parts
-// taking 6.)
+// taking 6.  More loads under way need registers that this kernel does not have.)
 #include "ffn_epilogue.h"
 #include "sample_internal.h"
 
