@@ -304,3 +304,76 @@ def test_rows_per_call(qll, B):
     x = torch.randn(B, V, generator=g, device="cuda") * 3
     u = torch.rand(B, generator=g, device="cuda").tolist()
     run(qll, x, u, B, **expand([dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.7), dict(min_p=0.02), dict(temperature=0.0)], B))
+
+
+# --------------------------------------------------------------------------
+# lists that start at any 4 bytes, outputs and workspaces of the caller
+# --------------------------------------------------------------------------
+
+def shifted(t, fill=0):
+    """A copy of t, contiguous, that starts 4 bytes past a 16-byte border."""
+    buf = torch.full((t.numel() + 9,), fill, dtype=t.dtype, device="cuda")
+    at = next(i for i in range(1, 5) if buf[i:].data_ptr() % 16 == 4)
+    out = buf[at:at + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("T,k", [(5, 4), (300, 8)])
+def test_lists_at_any_four_bytes(qll, T, k):
+    E, N, K = 16, 144, 160
+    g = gen(T)
+    logits, w = rnd(g, T, E, dtype=F32), experts(g, E, N, K)
+    want = qll.moe_route(logits, k, plan=True)
+    outs = [shifted(t, 7) for t in want]
+    for t in outs:
+        t.fill_(-9)
+    bias = rnd(g, E, dtype=F32)
+    for b in (None, bias):
+        want = qll.moe_route(logits, k, bias=b, plan=True)
+        ws = torch.empty(max(16, qll.load_library().qll_moe_sort_workspace_bytes(T, E, k)), dtype=torch.uint8, device="cuda")
+        got = qll.moe_route(logits, k, bias=None if b is None else shifted(b), plan=True, ids=outs[0], weights=outs[1],
+                            offsets=outs[2], rows=outs[3], places=outs[4], workspace=ws)
+        for a, o, t in zip(want, outs, got):
+            assert t is o and torch.equal(a, o)
+    ids, weights, offsets, rows, places = outs
+    for a, o in zip(want[2:], qll.moe_sort(ids, E, offsets=shifted(offsets), rows=shifted(rows), places=shifted(places))):
+        assert torch.equal(a, o)
+    dw = rnd(g, T, k, dtype=F32)
+    assert torch.equal(qll.moe_route_backward(logits, ids, shifted(dw)), qll.moe_route_backward(logits, want[0], dw))
+    x, sx = quant(rnd(g, T, K))
+    a = qll.gated_fp8_grouped(x, *w[:2], shifted(sx), *(shifted(s) for s in w[2:]), offsets, rows=rows)
+    assert torch.equal(a, qll.gated_fp8_grouped(x, *w[:2], sx, *w[2:], want[2], rows=want[3]))
+    y, dout = rnd(g, T * k, K), rnd(g, T, K)
+    assert torch.equal(qll.moe_combine(y, places, weights), qll.moe_combine(y, want[4], want[1]))
+    for p, q in zip(qll.moe_combine_backward(y, places, weights, dout, dweights=shifted(weights)),
+                    qll.moe_combine_backward(y, want[4], want[1], dout)):
+        assert torch.equal(p, q)
+    u = torch.rand(T, generator=g, device="cuda")
+    v = rnd(g, T, 501, dtype=F32)
+    kw = dict(temperature=u + 0.5, top_k=(u * 50).int(), top_p=1 - u / 4, min_p=u / 50)
+    want = qll.sample_tokens(v, u, probs=True, **kw)
+    got = qll.sample_tokens(v, shifted(u), probs=shifted(u), tokens=shifted(want[0]), **{n: shifted(t) for n, t in kw.items()})
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+def test_choices_of_one_expert(qll):
+    """Every token to the same few experts, and ids that name one twice."""
+    T, E, k = 3000, 128, 4
+    ids = torch.full((T, k), 77, dtype=I32, device="cuda")
+    ids[:, 1] = 3
+    offsets, rows, places = qll.moe_sort(ids, E)
+    flat = ids.reshape(-1).long()
+    by = torch.argsort(flat, stable=True)
+    same(rows, (by // k).int(), "rows")
+    same(places.reshape(-1)[by], torch.arange(T * k, dtype=I32, device="cuda"), "places")
+    assert offsets[77] == T and offsets[78] == T * k and offsets[3] == 0 and offsets[E] == T * k
+    # gradients of an expert that is named twice add up
+    logits = rnd(gen(5), 64, E, dtype=F32)
+    dw = rnd(gen(6), 64, k, dtype=F32)
+    d = qll.moe_route_backward(logits, ids[:64].contiguous(), dw, renormalize=False)
+    one = torch.tensor([[77, 3]], dtype=I32, device="cuda").repeat(64, 1)
+    both = torch.stack([dw[:, 0] + dw[:, 2] + dw[:, 3], dw[:, 1]], 1)
+    e = qll.moe_route_backward(logits, one, both, renormalize=False)
+    # (sums of the same terms in another order: a few roundings of their sizes)
+    assert ((d - e).abs() <= 16 * 2.0 ** -24 * dw.abs().sum(1, keepdim=True)).all()
