@@ -460,7 +460,8 @@ typedef enum {
  *   ids[t][0..topk): the experts of open groups with the largest c, in falling
  *     order; equal values go to the lower index, a NaN counts as -infinity
  *   weights[t][j] = scale * p, with renormalize scale * p / (sum of p over the
- *     chosen); the bias takes no part; 0 where that sum is 0
+ *     chosen); the bias takes no part; 0 where that sum is 0 (sigmoids of
+ *     logits of -700 and below are)
  * c is formed in 64 bits, so values that differ are told apart.  A row of
  * logits with a NaN or +infinity has NaN softmax weights (its ids are in range
  * and distinct all the same); one of -infinity alone has softmax weights 0.

@@ -41,6 +41,9 @@ __host__ __device__ constexpr int hist_stride(int E) { return (E + 3) / 4 * 4; }
 constexpr int kOneGroup = 1024;  // choices that one workgroup sorts
 constexpr float kNan = __builtin_nanf("");
 constexpr float kInf = __builtin_inff();
+// Sigmoids whose sum is below kDeep are e^x to 2^-50 and lose bits below
+// 2^-126; with the largest logit at kNothing or below they count as 0.
+constexpr float kDeep = 0x1p-56f, kNothing = -700.0f;
 
 // ---- wave reductions (lane 63 collects, every lane gets the result) ----
 
@@ -618,8 +621,15 @@ __global__ __launch_bounds__(WAVES * 64) void moe_route_kernel(RouteArgs a)
             else
                 w = bad ? kNan : (m > -kInf ? exp_f(l - m) : 0.0f);
         }
-        if (a.renorm)
+        if (a.renorm) {
             z = wave_sum(w);
+            // sigmoids next to nothing (kDeep): relative to the largest they are not
+            if (a.score == SCORE_SIGMOID && z < kDeep) {
+                m = wave_max(lane < k ? l : -kInf);
+                w = lane < k && m > kNothing ? exp_f(l - m) : 0.0f;
+                z = wave_sum(w);
+            }
+        }
         if (a.renorm || a.score == SCORE_SOFTMAX)
             w = w == 0.0f && z == 0.0f ? 0.0f : w / z;
         if (lane < k) {
@@ -710,7 +720,7 @@ __global__ __launch_bounds__(1024) void moe_place_kernel(SortArgs a)
 // dx of w = scale p[ids] (or renormalised), a wave per token:
 //   softmax      dx = p (dp - <dp, p>), dp = scale dw at the chosen
 //   renormalised the same over the chosen alone
-//   sigmoid      dx = dp p (1 - p), renormalised dp = (dw - <dw, r>) / sum p
+//   sigmoid      dx = dw p (1 - p), renormalised (dw - <dw, r>) r (1 - p)
 template <int VPL, bool BF16>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardArgs a)
 {
@@ -760,14 +770,20 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(RouteBackwardAr
         // p and p (1 - p) from e^-|x|: 1 - p would cancel where p is next to 1
         const float e = expf(-fabsf(xc));
         const float i = 1.0f / (1.0f + e);
-        const float s = live ? (xc < 0.0f ? e * i : i) : 0.0f;
-        g = dw;
         if (a.renorm) {
-            const float z = wave_sum(s);
-            const float iz = z == 0.0f ? 0.0f : 1.0f / z;
-            g = (dw - wave_sum(dw * (s * iz))) * iz;
+            float s = live ? (xc < 0.0f ? e * i : i) : 0.0f;
+            float z = wave_sum(s);
+            if (z < kDeep) {
+                const float m = wave_max(xc);
+                s = live && m > kNothing ? expf(xc - m) : 0.0f;
+                z = wave_sum(s);
+            }
+            const float r = z == 0.0f ? 0.0f : s / z;
+            g = r * (xc < 0.0f ? i : e * i) * (dw - wave_sum(dw * r));
+        } else {
+            g = dw * (e * i * i);
         }
-        g = live ? g * (e * i * i) : 0.0f;
+        g = live ? g : 0.0f;
     }
     float d[VPL];
 #pragma unroll

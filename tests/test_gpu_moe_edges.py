@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import moe_reference as ref  # noqa: E402
 from test_gpu_ffn import BF, D, F32, check, gen, guarded, qll, quant, rnd  # noqa: E402,F401
-from test_gpu_moe import I32, experts, gated_rows, same  # noqa: E402
+from test_gpu_moe import I32, INF, experts, gated_rows, same  # noqa: E402
 from test_gpu_sample import expand, run  # noqa: E402
 
 
@@ -377,3 +377,51 @@ def test_choices_of_one_expert(qll):
     e = qll.moe_route_backward(logits, one, both, renormalize=False)
     # (sums of the same terms in another order: a few roundings of their sizes)
     assert ((d - e).abs() <= 16 * 2.0 ** -24 * dw.abs().sum(1, keepdim=True)).all()
+
+
+@pytest.mark.parametrize("level", [-30.0, -38.0, -41.0, -60.0, -95.0, -150.0, -650.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sigmoids_next_to_nothing(qll, dtype, level):
+    """Renormalised sigmoids of logits far below zero are weights like any."""
+    T, E, k = 50, 96, 6
+    g = gen(int(-level))
+    x = (level + rnd(g, T, E, std=3.0, dtype=F32)).to(dtype)
+    ids, w = qll.moe_route(x, k, score="sigmoid")
+    order = torch.sort(x.to(D), dim=1, descending=True, stable=True).indices[:, :k]
+    same(ids, order.int(), "ids")
+    chosen = x.to(D).gather(1, order)
+    p = torch.sigmoid(chosen)
+    want = p / p.sum(1, keepdim=True)
+    # (the exponent's rounding, |x| 2^-24 where it is not relative to the largest)
+    far = torch.where(chosen < -36, chosen[:, :1] - chosen, -chosen.clamp(max=0)) + 3
+    far = far.clamp(min=0) + (-chosen).clamp(0, 42)
+    bound = (2 * far.amax(1, keepdim=True) + 40) * 2.0 ** -24
+    assert ((w.to(D) - want).abs() <= bound * want).all()
+    dw = rnd(g, T, k, dtype=F32)
+    dx = qll.moe_route_backward(x, ids, dw, score="sigmoid")
+    mag = want * torch.sigmoid(-chosen)
+    dot = (dw.to(D) * want).sum(1, keepdim=True)
+    got = dx.to(D).gather(1, order)
+    size = mag * (dw.to(D).abs() + (dw.to(D).abs() * want).sum(1, keepdim=True))
+    step = torch.finfo(dtype).eps / 2
+    assert ((got - mag * (dw.to(D) - dot)).abs() <= (2 * bound + step * 1.01) * size + 1e-37).all()
+    assert (dx.scatter(1, order, 0) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_experts_at_the_lowest_value(qll, dtype):
+    """A row of the type's lowest value: sigmoids and gradients are 0, softmax
+    weights even; a row with two other experts takes these first."""
+    x = torch.full((3, 40), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    x[1, 33], x[1, 5] = 1.0, 0.0
+    x[2] = -INF
+    ids, w = qll.moe_route(x, 4, score="sigmoid")
+    assert ids[0].tolist() == [0, 1, 2, 3] and ids[1].tolist() == [33, 5, 0, 1] and ids[2].tolist() == [0, 1, 2, 3]
+    assert (w[0] == 0).all() and (w[2] == 0).all() and (w[1, 2:] == 0).all()
+    p = torch.sigmoid(torch.tensor([1.0, 0.0], dtype=D, device="cuda"))
+    assert ((w[1, :2].to(D) - p / p.sum()).abs() <= 50 * 2.0 ** -24).all()
+    for renorm in (True, False):
+        dx = qll.moe_route_backward(x, ids, torch.ones_like(w), score="sigmoid", renormalize=renorm)
+        assert (dx[0] == 0).all() and (dx[2] == 0).all() and torch.isfinite(dx.float()).all()
+    w = qll.moe_route(x, 4)[1]
+    assert ((w[0] - 0.25).abs() <= 1e-6).all() and (w[2] == 0).all() and (w[1, 2:] == 0).all()
