@@ -33,8 +33,8 @@
 // A workgroup takes a row, or one of `parts` of it where there are few rows;
 // then a second launch adds the parts' bins and finishes.
 //
-// Measured: one row of 151936 bf16 logits in 16 parts 7.5 us, the second launch
-// 16 where the list holds the answer and up to 47 for a flat row under top-p;
+// Measured: one row of 151936 bf16 logits in 8 parts 9.8 us, the second launch
+// 13 where the list holds the answer and up to 44 for a flat row under top-p;
 // 256 fp32 rows of mixed options 93: 33 for the read (4.7 TB/s), then the
 // flattest row's second read 30 and its two searches 22; 48 rows of 50021 under
 // top-p 10 and 37.  Past the first read a row is a chain of short steps of one
@@ -1085,10 +1085,14 @@ hipError_t launch(const SampleArgs& a, hipStream_t stream)
 
 int sample_parts(int64_t B, int64_t V)
 {
-    // parts of 8192 values and more, as many as fill the compute units
-    const int64_t by_values = V / 8192, by_rows = B ? 256 / B : 1;
-    const int64_t n = by_values < by_rows ? by_values : by_rows;
-    return (int)(n < 1 ? 1 : (n > 16 ? 16 : n));
+    // Parts of 8192 values and more, as many as fill the compute units.  Past 8 of
+    // them, of 32768 and more: each part costs the second launch 0.4 us (a row
+    // of 151936 in 8, 11 and 16 parts: 9.8 + 12.7 us, 8.5 + 14.6, 7.5 + 15.9).
+    const int64_t by_values = V / 8192, by_rows = B ? 256 / B : 1, by_join = V / 32768;
+    const int64_t most = by_join < 8 ? 8 : (by_join > 16 ? 16 : by_join);
+    int64_t n = by_values < by_rows ? by_values : by_rows;
+    n = n > most ? most : n;
+    return (int)(n < 1 ? 1 : n);
 }
 int64_t sample_part_bytes() { return (int64_t)sizeof(Part); }
 
