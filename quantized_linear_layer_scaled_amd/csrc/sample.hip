@@ -603,13 +603,14 @@ struct Sampler {
         if (threadIdx.x < kFew)
             rank[threadIdx.x] = 0;
         __syncthreads();
-        // four threads per value share the comparisons
-        const int i = threadIdx.x & (kFew - 1), part = threadIdx.x / kFew;
-        constexpr int EACH = kFew / (kThreads / kFew);
+        // 4, 8 or 16 threads per value share the comparisons
+        const int wide = n <= 64 ? 6 : (n <= 128 ? 7 : 8);
+        const int i = threadIdx.x & ((1 << wide) - 1), part = threadIdx.x >> wide;
         const uint64_t mine = i < n ? s.list[i] : 0;
         if ((i & ~63) < n) {
             uint32_t r = 0;
-            for (int j = part * EACH; j < min(n, (part + 1) * EACH); ++j)
+#pragma unroll 4
+            for (int j = part; j < n; j += kThreads >> wide)
                 r += s.list[j] < mine;
             if (r)
                 atomicAdd(&rank[i], r);
