@@ -34,10 +34,10 @@
 // then a second launch adds the parts' bins and finishes.
 //
 // Measured: one row of 151936 bf16 logits in 8 parts 9.8 us, the second launch
-// 13 where the list holds the answer and up to 44 for a flat row under top-p;
-// 256 fp32 rows of mixed options 93: 33 for the read (4.7 TB/s), then the
-// flattest row's second read 30 and its two searches 22; 48 rows of 50021 under
-// top-p 10 and 37.  Past the first read a row is a chain of short steps of one
+// 13 where the list holds the answer and up to 42 for a flat row under top-p;
+// 256 fp32 rows of mixed options 85: 33 for the read (4.7 TB/s), then the
+// flattest row's second read 30 and its two searches 16; 48 rows of 50021 under
+// top-p 10 and 33.  Past the first read a row is a chain of short steps of one
 // workgroup.  (The second read over as many workgroups as the first: 26 us in
 // place of 36 for one row, but 29 in place of 21 for 48, the joining of the parts
 // taking 6.  More loads under way need registers that this kernel does not have.)
@@ -686,8 +686,10 @@ struct Sampler {
             }
             scan_threads(s, c, w, ca, wa);
             // the first of them where the search ends, else the last that holds any
+            // (one thread of a wave names its)
             uint32_t before_c[PER];
             double before_w[PER];
+            int first = -1, last = -1;
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
                 before_c[e] = c;
@@ -695,11 +697,17 @@ struct Sampler {
                 c += mine_c[e];
                 w += mine_w[e];
                 if (mine_c[e]) {
-                    if (past(count + c, weight + w))
-                        atomicMin(&s.found, (int)threadIdx.x * PER + e);
-                    atomicMax(&s.n, (uint32_t)(threadIdx.x * PER + e));
+                    if (first < 0 && past(count + c, weight + w))
+                        first = (int)threadIdx.x * PER + e;
+                    last = (int)threadIdx.x * PER + e;
                 }
             }
+            const int lane = threadIdx.x & 63;
+            const uint64_t firsts = __ballot(first >= 0), lasts = __ballot(last >= 0);
+            if (firsts && lane == __ffsll((long long)firsts) - 1)
+                atomicMin(&s.found, first);
+            if (lasts && lane == 63 - __clzll((long long)lasts))
+                atomicMax(&s.n, (uint32_t)last);
             __syncthreads();
             const int found = uniform(s.found < kSub ? s.found : (int)s.n);
 #pragma unroll
