@@ -442,6 +442,8 @@ struct Experts {
         }
         if (a.group_best > 1 && size > 1)
             first += second;
+        // (+infinity and -infinity, of biases, are no number: below all others)
+        first = first == first ? first : none;
         // a group's rank: how many are better, or as good and before it
         const int step = lanes ? lanes : 1;  // lanes from group to group
         int rank = 0;

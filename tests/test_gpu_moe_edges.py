@@ -84,6 +84,38 @@ def test_masked_experts_with_a_bias(qll):
             assert ((w.cpu().to(D) - rw).abs() <= bound + 1e-37).all()
 
 
+# experts of a token and groups: groups of a lane, of several lanes, of none's
+# multiple, of more experts than a lane holds
+BIASED = [(32, 32, 8, 5), (64, 8, 3, 6), (96, 4, 2, 9), (250, 5, 2, 7), (256, 8, 4, 8), (1000, 8, 3, 8)]
+
+
+@pytest.mark.parametrize("E,groups,keep,k", BIASED)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_infinite_biases(qll, score, E, groups, keep, k):
+    """Experts that are always and never chosen, together in a group: +infinity
+    and -infinity add up to no number, which counts as -infinity."""
+    T, size = 50, E // groups
+    g = gen(E)
+    x = rnd(g, T, E, dtype=F32)
+    bias = rnd(g, E, std=0.1, dtype=F32)
+    rand = torch.rand(E, generator=g, device="cuda")
+    bias[rand < 0.2] = -INF
+    mixed = bias.clone()
+    for at in (0, groups // 2, groups - 1):  # one of +infinity, the rest out
+        mixed[at * size:(at + 1) * size] = -INF
+        mixed[at * size + size // 2] = INF
+    mixed[size:2 * size] = INF
+    out = torch.full_like(bias, -INF)  # one group left
+    out[-size:] = bias[-size:]
+    for b in (bias, mixed, out, -mixed):
+        for best in (1, 2):
+            kw = dict(score=score, bias=b, groups=groups, topk_groups=keep, group_best=best)
+            ids, w = qll.moe_route(x, k, **kw)
+            rid, rw, bound = ref.route(x, k, **kw)
+            same(ids, rid, (score, best))
+            assert ((w.cpu().to(D) - rw).abs() <= bound + 1e-37).all()
+
+
 def test_far_chosen_experts(qll):
     """Renormalised weights of experts far below the largest logit, which lies
     in a group that is not open."""
