@@ -518,8 +518,9 @@ struct Sampler {
     // The keys of the bins b0 .. b1.
     __device__ __forceinline__ void keys_of(int b0, int b1, uint32_t& from, uint32_t& to) const
     {
-        auto first = [&](int b) {  // the least key of bin b or one before
-            return least_key(scale.ref - (b + 1 - kAbove) / scale.per, key_of(kMax), [&](uint32_t key) {
+        // the least key of bin b or one before, infinity's if no value lies there
+        auto first = [&](int b) {
+            return least_key(scale.ref - (b + 1 - kAbove) / scale.per, key_of(kInf), [&](uint32_t key) {
                 return scale.steps(value_of(key)) < (double)(b + 1);
             });
         };

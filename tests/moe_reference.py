@@ -188,6 +188,7 @@ def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         w = (xs == math.inf).to(D)
     else:
         w = torch.where(xs == m, torch.ones_like(xs), torch.exp((xs - m) / temperature))
+        w = torch.where(xs == -math.inf, torch.zeros_like(xs), w)  # (-inf / inf is no number)
     n = len(x)
     if 0 < top_k < n:
         n = top_k

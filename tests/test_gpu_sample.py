@@ -134,6 +134,29 @@ def test_rows_that_are_not_finite(qll):
         run(qll, x[:2], [0.5, NAN], opts, **expand(opts, 2))
 
 
+@pytest.mark.parametrize("V", [8000, 20011])
+def test_rows_with_the_largest_value(qll, V):
+    """The type's largest value, once among rows that are masked in part, many
+    times, or in every place: a number like any other."""
+    opts = [dict(), dict(top_k=5), dict(top_k=V // 3), dict(top_p=0.5), dict(min_p=0.3), dict(top_p=0.9, min_p=0.5),
+            dict(temperature=INF), dict(temperature=INF, top_k=V - 3), dict(temperature=INF, top_p=0.75), dict(temperature=0.0)]
+    B = len(opts)
+    u = [(i + 0.5) / B for i in range(B)]
+    for dtype in (F32, BF):
+        x, _ = rows(V, B, V, dtype)
+        top = torch.finfo(dtype).max
+        x[:, 1000] = top
+        kinds = [x, x.clone(), x.clone(), torch.full_like(x, top), torch.full_like(x, top)]
+        kinds[1][:, :V // 4] = -INF
+        kinds[1][:, V - 1] = top
+        kinds[2][:, ::2] = top
+        kinds[4][:, 1::3] = -top
+        for i, t in enumerate(kinds):
+            run(qll, t, u, (V, i), **expand(opts, B))
+            run(qll, t, [0.0] * B, (V, i), **expand(opts, B))
+            run(qll, t, [1.0 - 2.0 ** -24] * B, (V, i), **expand(opts, B))
+
+
 def test_random_numbers_at_the_ends(qll):
     """0, the last value below 1, and what is no random number at all."""
     x, _ = rows(9, 6, 2000, F32)
