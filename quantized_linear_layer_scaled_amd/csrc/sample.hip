@@ -213,7 +213,7 @@ struct Scale {
     }
     static __device__ __forceinline__ bool inside(double y)
     {
-        return fabs(y - kBins / 2) < kBins / 2;  // (0 is outside)
+        return fabs(y - kBins / 2) < kBins / 2;  // (0 to 1e-13 is outside)
     }
     // the bin of a value, -1 for none
     __device__ __forceinline__ int bin(float x) const
@@ -914,7 +914,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a)
     // (the list is there)
     for (bool again = MODE == JOIN; ; again = true) {
         if (again) {
-            if (greedy || !(m < kInf) || m == -kInf || sc.steps(m) > 0.0)
+            if (greedy || !(m < kInf) || m == -kInf || Scale::inside(sc.steps(m)))
                 break;
             sc.ref = uniform((double)m);
         }

@@ -157,6 +157,52 @@ def test_rows_with_the_largest_value(qll, V):
             run(qll, t, [1.0 - 2.0 ** -24] * B, (V, i), **expand(opts, B))
 
 
+def run_small_weights(qll, x, u, what, **kw):
+    """As run, for rows that have weights below e^-31.9, which may be taken as 0.
+    Their sum `gone` moves a sum over all weights to anywhere in [z - gone, z],
+    and a bin's weight is off by up to 2^-37 of itself (err).  The kept front then
+    ends at the first token whose sum reaches p z or p (z - gone), and the token
+    is one of those between the first sums past u times the least and the most
+    that is kept."""
+    t = {k: torch.tensor(v, dtype=I32 if k == "top_k" else F32, device="cuda") for k, v in kw.items()}
+    ut = torch.tensor(u, dtype=F32, device="cuda")
+    tokens, probs = qll.sample_tokens(x, ut, probs=True, **t)
+    for b in range(x.shape[0]):
+        k, p, m = (t[n][b].item() for n in ("top_k", "top_p", "min_p"))
+        xs, order = torch.sort(x[b].cpu().double(), descending=True, stable=True)
+        w = torch.exp((xs - xs[0]) / t["temperature"][b].item())
+        n = k if 0 < k < len(w) else len(w)
+        c = torch.cumsum(w, 0)
+        gone, err = float(w[:n][w[:n] < math.exp(-31.9)].sum()), 2.0 ** -37 * float(c[n - 1])
+        first = lambda v: min(int((c < v).sum()), n - 1)  # noqa: E731
+        ends = [n - 1, n - 1] if p >= 1 else [first(p * (c[n - 1] - gone) - err), first(p * c[n - 1] + err)]
+        if m > 0:
+            ends = [min(e, int((w >= m).sum()) - 1) for e in ends]
+        least, most = (float(c[ends[0]]) - gone - err) * ut[b].item(), (float(c[ends[1]]) + err) * ut[b].item()
+        at = int((order == tokens[b].item()).nonzero())
+        assert min(int((c <= least - err).sum()), ends[0]) <= at <= min(int((c <= most + err).sum()), ends[1]), (what, b, u[b], at)
+        share = float(w[at] / c[ends[1]])
+        assert abs(probs[b].item() - share) <= 2.0 ** -22 * share + 1e-30, (what, b, u[b], probs[b].item(), share)
+
+
+@pytest.mark.parametrize("temp,above", [(0.75, 12.0234375), (1.5, 24.046875), (3.0, 48.09375), (0.375, 6.01171875)])
+def test_maximum_at_the_border_of_the_first_bin(qll, temp, above):
+    """A maximum outside the sample that lies 1026 / 64 temperatures above the
+    sample's, in exact numbers; the rounded inverse temperature puts it a last
+    bit inside of the first bin."""
+    V = 20011
+    check = run if (above + 8) / temp < 31.9 else run_small_weights
+    for B in (1, 3, 140):
+        g = gen(B)
+        x = -torch.rand(B, V, generator=g, device="cuda") * 8
+        x[:, ::100] = 0.0
+        x[:, 4500] = above
+        for o in (dict(), dict(top_k=50), dict(top_p=0.9), dict(min_p=1e-7), dict(top_p=0.99999995, top_k=9000)):
+            kw = expand([dict(o, temperature=temp)], B)
+            check(qll, x, torch.rand(B, generator=g, device="cuda").tolist(), (B, o), **kw)
+            check(qll, x, [1.0 - 2.0 ** -24] * B, (B, o), **kw)
+
+
 def test_random_numbers_at_the_ends(qll):
     """0, the last value below 1, and what is no random number at all."""
     x, _ = rows(9, 6, 2000, F32)
