@@ -118,7 +118,8 @@ __device__ __forceinline__ float exp_f(float z)
     return __builtin_amdgcn_exp2f(z * 1.442695041f);
 }
 
-// 2^y for |y| <= 1000, to 2^-51 of itself: the Taylor series of the fraction.
+// 2^y for |y| <= 1000, to 2^-51 of itself, and 0 for -1100: the Taylor series of
+// the fraction.
 // (The library's exp and division take three times as many instructions; a
 // wave forms a value per expert.)
 __device__ __forceinline__ double pow2(double y)
@@ -474,7 +475,7 @@ __device__ __forceinline__ int exact_choice(const RouteArgs& a, const Experts<VP
         double sum = 0.0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const double e = pow2(fmax(((double)x[v] - (double)m) * kLog2e, -1000.0));
+            const double e = pow2(fmax(((double)x[v] - (double)m) * kLog2e, -1100.0));
             c[v] = x[v] > -kInf ? e : 0.0;
             sum += c[v];
         }

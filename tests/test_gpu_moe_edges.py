@@ -116,6 +116,21 @@ def test_infinite_biases(qll, score, E, groups, keep, k):
             assert ((w.cpu().to(D) - rw).abs() <= bound + 1e-37).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_masked_in_two_ways(qll, score, dtype):
+    """A group of -infinity and one of the type's lowest value both have scores
+    of 0 in 64 bits: the first of them is open."""
+    x = rnd(gen(8), 12, 32, dtype=dtype)
+    x[:, :8] = -INF
+    x[:, 16:24] = torch.finfo(dtype).min
+    for best in (1, 2):
+        for flip in (x, x.flip(1)):
+            flip = flip.contiguous()
+            kw = dict(score=score, groups=4, topk_groups=3, group_best=best)
+            same(qll.moe_route(flip, 20, **kw)[0], ref.route(flip, 20, **kw)[0], (score, best))
+
+
 def test_far_chosen_experts(qll):
     """Renormalised weights of experts far below the largest logit, which lies
     in a group that is not open."""
