@@ -584,11 +584,14 @@ __global__ __launch_bounds__(WAVES * 64) void moe_route_kernel(RouteArgs a)
             for (int v = 0; v < VPL; ++v)
                 c[v] += ex.bias[v];
             if (grouped) {
-                // (the sums' roundings, of four values and two sums)
+                // (the sums' roundings, of four values and two sums; an infinite
+                // value, from a bias, has none: 25 us with one such bias for the
+                // prompt above, as without, and 37 where every token is formed again,
+                // as with one of -1e9)
                 float most = 0.0f;
 #pragma unroll
                 for (int v = 0; v < VPL; ++v)
-                    most = fmaxf(most, fabsf(c[v]));
+                    most = fmaxf(most, fabsf(c[v]) < kInf ? fabsf(c[v]) : 0.0f);
                 const float group_error = 0x1p-20f * wave_max(most);
                 float margin;
                 open = ex.open(a, c, (float*)group_value[wave], margin);

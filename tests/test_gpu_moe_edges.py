@@ -116,6 +116,25 @@ def test_infinite_biases(qll, score, E, groups, keep, k):
             assert ((w.cpu().to(D) - rw).abs() <= bound + 1e-37).all()
 
 
+@pytest.mark.parametrize("E,groups,keep,k", BIASED)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_close_groups_beside_experts_out_of_service(qll, score, E, groups, keep, k):
+    """Groups whose values 32 bits cannot tell apart, with biases of -infinity,
+    of the lowest value and of large sizes among them."""
+    T = 40
+    g = gen(E + k)
+    steps = torch.randint(0, 6, (T, E), generator=g, device="cuda")
+    x = 1.0 + steps * 2.0 ** -23
+    x[::4] = 1.0 + steps[::4] * 2.0 ** -16
+    bias = torch.randint(0, 3, (E,), generator=g, device="cuda") * 1e-8
+    gone = torch.rand(E, generator=g, device="cuda") < 0.3
+    for level in (-INF, torch.finfo(F32).min, -1e9, INF):
+        for best in (1, 2):
+            kw = dict(score=score, bias=torch.where(gone, level, bias).float(), groups=groups, topk_groups=keep, group_best=best)
+            ids, _ = qll.moe_route(x, k, **kw)
+            same(ids, ref.route(x, k, **kw)[0], (level, best))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_groups_masked_in_two_ways(qll, score, dtype):
