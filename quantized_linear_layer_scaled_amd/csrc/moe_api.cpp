@@ -12,7 +12,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x3FFFFF00;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxRowBytes = (((int64_t)1 << 31) - 1) / 256;
-constexpr int64_t kMaxChoices = (int64_t)1 << 26;  // a launch has 64 threads for each
+constexpr int64_t kMaxChoices = (int64_t)1 << 26;  // (twice kLaunchWaves)
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 

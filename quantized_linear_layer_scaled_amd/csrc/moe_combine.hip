@@ -167,12 +167,21 @@ hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t stream)
 
 hipError_t launch_moe_combine_backward(const CombineArgs& a, hipStream_t stream)
 {
-    const int64_t blocks = ((int64_t)a.T * a.k + 3) / 4;
-    if (a.fp32)
-        moe_combine_backward_kernel<true><<<(unsigned)blocks, 256, 0, stream>>>(a);
-    else
-        moe_combine_backward_kernel<false><<<(unsigned)blocks, 256, 0, stream>>>(a);
-    return hipGetLastError();
+    const int most = kLaunchWaves / a.k;  // tokens of a launch
+    const auto kernel = a.fp32 ? moe_combine_backward_kernel<true> : moe_combine_backward_kernel<false>;
+    hipError_t rc = hipSuccess;
+    for (int t = 0; t < a.T && rc == hipSuccess; t += most) {
+        CombineArgs b = a;
+        const size_t choice = (size_t)t * a.k;
+        b.places = a.places + choice;
+        b.weights = a.weights ? a.weights + choice : nullptr;
+        b.dweights = a.dweights ? a.dweights + choice : nullptr;
+        b.dout = (const char*)a.dout + (size_t)t * a.K * (a.fp32 ? 4 : 2);
+        b.T = a.T - t < most ? a.T - t : most;
+        kernel<<<(unsigned)(((int64_t)b.T * a.k + 3) / 4), 256, 0, stream>>>(b);
+        rc = hipGetLastError();
+    }
+    return rc;
 }
 
 }  // namespace qll

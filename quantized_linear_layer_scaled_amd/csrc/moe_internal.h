@@ -11,6 +11,9 @@ enum Score : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_COUNT };
 
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopk = 64;
+// Waves of a launch that has one for each token or choice (a launch holds fewer
+// than 2^32 threads); more of them take another launch, or a longer loop.
+constexpr int kLaunchWaves = 1 << 25;
 
 // The rows sorted by expert, for T x k choices (entry i = token i / k).
 struct SortArgs {

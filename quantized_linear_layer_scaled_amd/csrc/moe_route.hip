@@ -864,8 +864,9 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream)
         constexpr bool BF16 = decltype(B)::value;
         if (!s.offsets) {
             RouteArgs b = a;
-            b.sort.chunk = 4;
-            moe_route_kernel<VPL, BF16, 4, PLAN_NONE><<<(s.T + 3) / 4, 256, 0, stream>>>(b);
+            b.sort.chunk = s.T > kLaunchWaves ? 8 : 4;
+            moe_route_kernel<VPL, BF16, 4, PLAN_NONE>
+                <<<(s.T + b.sort.chunk - 1) / b.sort.chunk, 256, 0, stream>>>(b);
         } else if (!s.hist) {
             // (the groups' values of 16 waves would not fit in LDS)
             constexpr int WAVES = VPL >= 16 ? 8 : 16;
@@ -899,8 +900,20 @@ hipError_t launch_moe_sort(const SortArgs& a, hipStream_t stream)
 hipError_t launch_moe_route_backward(const RouteBackwardArgs& a, hipStream_t stream)
 {
     return with_logits(a.E, a.bf16, [&](auto V, auto B) {
-        moe_route_backward_kernel<decltype(V)::value, decltype(B)::value><<<(a.T + 3) / 4, 256, 0, stream>>>(a);
-        return hipGetLastError();
+        constexpr bool BF16 = decltype(B)::value;
+        hipError_t rc = hipSuccess;
+        for (int t = 0; t < a.T && rc == hipSuccess; t += kLaunchWaves) {
+            RouteBackwardArgs b = a;
+            const size_t row = (size_t)t * a.E * (BF16 ? 2 : 4);
+            b.logits = (const char*)a.logits + row;
+            b.dlogits = (char*)a.dlogits + row;
+            b.ids = a.ids + (size_t)t * a.k;
+            b.dweights = a.dweights + (size_t)t * a.k;
+            b.T = a.T - t < kLaunchWaves ? a.T - t : kLaunchWaves;
+            moe_route_backward_kernel<decltype(V)::value, BF16><<<(b.T + 3) / 4, 256, 0, stream>>>(b);
+            rc = hipGetLastError();
+        }
+        return rc;
     });
 }
 

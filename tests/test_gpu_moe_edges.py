@@ -278,6 +278,48 @@ def test_sample_past_32_bits(qll):
     assert torch.equal(t[:9].long(), torch.floor(u[:9].to(D) * V).long())
 
 
+# tokens and choices whose waves fill 2^32 threads, or all but a few, and one
+# more than a launch takes
+@pytest.mark.parametrize("T,k", [(1 << 26, 1), ((1 << 26) - 3, 1), ((1 << 26) // 3, 3), ((1 << 25) + 1, 1)])
+def test_most_choices(qll, T, k):
+    E, K = 4, 8
+    g = gen(k)
+    x = torch.randint(-8, 8, (T, E), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    ids, w = qll.moe_route(x, k, score="sigmoid", renormalize=False)
+    key = x.to(torch.int8) * 4 + (3 - torch.arange(E, dtype=torch.int8, device="cuda"))  # in order, ties too
+    order = torch.empty_like(ids)
+    for j in range(k):
+        best = key.amax(1, keepdim=True)
+        order[:, j:j + 1] = 3 - (best & 3)
+        key = torch.where(key == best, -128, key)
+    assert torch.equal(ids, order)
+    # (logits of 16 values: a weight and a slope each, off by a few u; u = 2^-24)
+    v = torch.arange(-8, 8, device="cuda", dtype=D)
+    p = torch.sigmoid(v)
+    at = x.gather(1, order.long()).long() + 8
+    assert ((w - p[at].float()).abs() <= 40 * 2.0 ** -24 * w).all()
+    dw = torch.randint(1, 3, (T, k), generator=g, device="cuda", dtype=torch.int8).float()
+    dx = qll.moe_route_backward(x, ids, dw, score="sigmoid", renormalize=False)
+    want = torch.zeros(T, E, device="cuda").scatter_(1, order.long(), dw * (p * torch.sigmoid(-v))[at].float())
+    # (and the bf16 output's half step, 2^-8)
+    assert ((dx.float() - want).abs() <= (2.0 ** -8 + 80 * 2.0 ** -24) * want).all()
+    del x, key, dx, want, order, at
+    planned = qll.moe_sort(ids, E)
+    flat = ids.reshape(-1)
+    assert torch.equal(planned[0][1:], torch.bincount(flat, minlength=E).cumsum(0).int())
+    expert = torch.bucketize(planned[2].reshape(-1), planned[0][1:], right=True)
+    assert torch.equal(expert.int(), flat)  # (each choice in its expert's rows)
+    assert torch.equal(planned[1][planned[2].long()], torch.arange(T, device="cuda", dtype=I32)[:, None].expand(T, k))
+    places = planned[2]
+    y = torch.randint(-4, 5, (T * k, 1), generator=g, device="cuda", dtype=torch.int8).to(BF).repeat(1, K)
+    dout = torch.randint(-4, 5, (T, 1), generator=g, device="cuda", dtype=torch.int8).to(BF).repeat(1, K)
+    # (small whole numbers: every product and sum is exact)
+    dy, got = qll.moe_combine_backward(y, places, dw, dout)
+    assert torch.equal(got, K * dout[:, :1].float() * y[:, 0].float()[places.long()])
+    assert torch.equal(dy[:, 0][places.long()], (dw * dout[:, :1]).to(BF))
+    assert torch.equal(dy[:, 0], dy[:, K - 1])
+
+
 # --------------------------------------------------------------------------
 # two at once
 # --------------------------------------------------------------------------
