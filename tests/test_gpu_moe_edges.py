@@ -177,7 +177,7 @@ def spread(E, R, g):
     return torch.bincount(torch.multinomial(p, R, True, generator=g), minlength=E).tolist()
 
 
-# few rows and tiles; tiles of 64x32, 64x64, 128x128 and 256x128 outputs
+# tiles of 64x32, 64x64, 128x128 and 256x128 outputs
 KERNELS = [(130, 300, 40, 144), (70, 40, 264, 272), (24, 100, 520, 160), (8, 80, 4104, 144), (130, 900, 1032, 80),
            (6, 700, 2056, 400), (70, 4000, 520, 272), (4, 2100, 4104, 144), (70, 14100, 264, 80), (3, 1500, 6001, 336)]
 
@@ -195,6 +195,32 @@ def test_gated_kernels(qll, E, R, N, K):
         whole, o = guarded(R, N, BF if out == "bf16" else F32)
         qll.gated_fp8_grouped(x, *w[:2], sx, *w[2:], offsets, rows=rows, out_dtype=out, out=o)
         check(o, gated_rows(x, sx, *w, offsets.tolist(), rows, "silu", out), (E, R, N, K, out), whole)
+    o2 = qll.gated_fp8_grouped(x[rows.long()], *w[:2], sx[rows.long()], *w[2:], offsets, out_dtype="fp32")
+    assert torch.equal(o, o2)
+
+
+# more than 64 experts in the kernel for few rows and tiles (one row an expert or
+# none, more rows than a block of 16); more than 1024, which the 256x128 tile's
+# list of experts does not hold, in that one and in tiles of 64x64 and 128x128
+MANY = [(70, 40, 40, 144), (130, 70, 9, 272), (65, 60, 64, 48), (1100, 90, 24, 160), (2000, 40, 40, 80),
+        (1100, 900, 72, 80), (1100, 60000, 264, 48), (1100, 220000, 40, 16)]
+
+
+@pytest.mark.parametrize("E,R,N,K", MANY)
+def test_gated_kernels_of_many_experts(qll, E, R, N, K):
+    g = gen(E + R + N + K)
+    counts = spread(E, R, g)
+    if R < 100:  # (an expert with several tiles of rows, behind the first 64)
+        counts = [0] * E
+        counts[E - 3], counts[E - 1], counts[66 if E > 69 else 1] = R // 2, R // 4, R - R // 2 - R // 4
+    T = 50
+    x, sx = quant(rnd(g, T, K))
+    w = experts(g, E, N, K)
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+    rows = torch.randint(0, T, (R,), generator=g, device="cuda", dtype=I32)
+    whole, o = guarded(R, N, F32)
+    qll.gated_fp8_grouped(x, *w[:2], sx, *w[2:], offsets, rows=rows, out_dtype="fp32", out=o)
+    check(o, gated_rows(x, sx, *w, offsets.tolist(), rows, "silu", "fp32"), (E, R, N, K), whole)
     o2 = qll.gated_fp8_grouped(x[rows.long()], *w[:2], sx[rows.long()], *w[2:], offsets, out_dtype="fp32")
     assert torch.equal(o, o2)
 
@@ -248,6 +274,32 @@ def test_gated_weights_past_32_bits(qll, counts):
     y, e = gated_rows(x, sx, w[0][-2:, cols], w[1][-2:, cols], s[0][-2:, cols], s[1][-2:, cols], [0, counts[0], sum(counts)],
                       rows, "silu", "bf16")
     check(o[:, cols], (y, e), counts)
+
+
+# (the test above has few rows an expert on average: one kernel, tiles of 64x64.)
+# Tiles of 128x128, from 48 rows an expert on, and 256x128, from 192 on
+@pytest.mark.parametrize("counts", [(900, 861), (3500, 3471)])
+def test_gated_weights_past_32_bits_in_large_tiles(qll, counts):
+    E, N, K = 36, 8192, 16384  # 128 MiB an expert: the last two start past 4 GiB
+    g = gen(3)
+    w = [torch.zeros(E, N, K, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    s = [torch.ones(E, N, device="cuda") for _ in range(2)]
+    for e in (E - 2, E - 1):
+        for a, b in zip(w, s):
+            a[e], b[e] = quant(rnd(g, N, K, std=0.05))
+    x, sx = quant(rnd(g, 20, K))
+    offsets = torch.zeros(E + 1, dtype=I32, device="cuda")
+    offsets[E - 1:] = torch.tensor([counts[0], sum(counts)], dtype=I32, device="cuda")
+    rows = torch.randint(0, 20, (sum(counts),), generator=g, device="cuda", dtype=I32)
+    o = qll.gated_fp8_grouped(x, *w, sx, *s, offsets, rows=rows)
+    cols = torch.randint(0, N, (64,), generator=g, device="cuda")
+    y, e = gated_rows(x, sx, w[0][-2:, cols], w[1][-2:, cols], s[0][-2:, cols], s[1][-2:, cols], [0, counts[0], sum(counts)],
+                      rows, "silu", "bf16")
+    check(o[:, cols], (y, e), counts)
+    # rows of one token and one expert are equal, in every column
+    for a, b in ((0, counts[0]), (counts[0], sum(counts))):
+        first = torch.stack([(rows[a:b] == t).int().argmax() + a for t in range(20)])
+        assert torch.equal(o[a:b], o[first[rows[a:b].long()]])
 
 
 def test_combine_past_32_bits(qll):
