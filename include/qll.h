@@ -455,14 +455,17 @@ typedef enum {
 
 /* Routing.  With c = p + bias, or the logits themselves without a bias:
  *   groups: the experts come in `groups` runs of E / groups; a group's value is
- *     the sum of its group_best (1 or 2) largest p + bias, and the topk_groups
- *     groups of the largest values are open (all of them: topk_groups = groups)
+ *     the sum of its group_best (1 or 2) largest p + bias (biases may be infinite;
+ *     a sum that is no number counts as -infinity), and the topk_groups groups of
+ *     the largest values are open (all of them: topk_groups = groups)
  *   ids[t][0..topk): the experts of open groups with the largest c, in falling
  *     order; equal values go to the lower index, a NaN counts as -infinity
  *   weights[t][j] = scale * p, with renormalize scale * p / (sum of p over the
  *     chosen); the bias takes no part; 0 where that sum is 0 (sigmoids of
- *     logits of -700 and below are)
- * c is formed in 64 bits, so values that differ are told apart.  A row of
+ *     logits of -700 and below are; softmax scores are taken relative to the
+ *     largest chosen one, so that their sum is 0 for -infinity alone)
+ * c is formed in 64 bits, so values that differ are told apart (a sigmoid below
+ * 2^-1000 is taken as 2^-1000).  A row of
  * logits with a NaN or +infinity has NaN softmax weights (its ids are in range
  * and distinct all the same); one of -infinity alone has softmax weights 0.
  *   logits bf16 or fp32 [T][E] (logits_dtype, QLL_OUT_BF16 or _FP32); bias fp32
@@ -500,6 +503,8 @@ int64_t qll_moe_sort_workspace_bytes(int64_t T, int64_t E, int64_t topk);
  *   out[i][n] = act(g) u,  t = rows[i] (rows NULL: t = i, R = T),
  *   g = (sum_k A[t][k] Bg[e][n][k]) sa[t] sg[e][n],  u likewise with Bu, su,
  *   e the expert that owns row i
+ *   (sums as in gated_fp8: the matrix core's e4m3 steps, off by up to 2^-12 of
+ *   the terms' magnitudes)
  *   A e4m3 [T][K]; Bg, Bu e4m3 [E][N][K]; sa fp32 [T]; sg, su fp32 [E][N];
  *   offsets int32 [E + 1], read as gemm_fp8_grouped reads them (rows that no
  *   expert owns are left unwritten); rows int32 [R]: a token outside [0, T)

@@ -9,9 +9,13 @@
 // A wave routes a token: lane l holds the VPL experts l VPL .. of it in
 // registers.  Values become unsigned keys of the same order, 0 for none, and
 // the k largest come out one by one, each a maximum over the wave.  Bound by
-// the vector instructions of these maxima (about 30 for 256 experts, 4 cycles
-// each), not by the logits: 8191 tokens, 256 experts, top-8, fp32: softmax 11 us,
-// 7.2 of it with top-1; sigmoid with a bias 13.5, and with 4 of 8 groups 17.
+// the chain of these maxima (six DPP steps, a ballot and two lane reads, each
+// behind the one before), not by the logits: 8191 tokens, 256 experts, top-8,
+// fp32: softmax 11 us, 7.2 of it with top-1; sigmoid with a bias 13.5, and with
+// 4 of 8 groups 17.5, where vector instructions take 45% of the SIMDs' cycles.
+// Few experts leave lanes idle (8192 tokens of 8, top-2: 6 us).  512 experts with
+// a plan have 16 waves of 128 registers and spill 15 to 27 more: 20 us with top-8,
+// against 16 without a plan, in 4 waves of 164.
 //
 // A choice is right or wrong, so values next to each other have to be told
 // apart.  Without a bias the logits themselves are compared.  With one the sums
@@ -26,8 +30,9 @@
 // every workgroup counts its chunk of tokens, and a second launch adds the
 // counts before its own chunks and places the choices 64 at a time, equal
 // experts of a wave being found by comparing the bits of their numbers over
-// the lanes (65528 choices of 256 experts: 8.4 us).  Up to kOneGroup choices a
-// single workgroup does everything (one token, 64 experts, top-8: 5.1 us).
+// the lanes (65528 choices of 256 experts: 8.5 us, by 64 workgroups that each read
+// all counts; counting them in a launch of its own 2.9).  Up to kOneGroup choices
+// a single workgroup does everything (one token, 64 experts, top-8: 5.3 us).
 #include "ffn_epilogue.h"
 #include "moe_internal.h"
 
@@ -224,7 +229,9 @@ __device__ __forceinline__ float key_value(uint32_t key)
 }
 // Whether two of the first n picks, one after the other, or the last of them
 // and the next, are closer than their errors: `error`, and 2^-22 of either's
-// size.  (A lane without a pick has key 0.)
+// size.  (A lane without a pick has key 0.  The pick behind lane 63's is not known
+// and counts as close: topk = 64 with a bias goes on in 64 bits, 24 us for 1024
+// tokens of 256 experts, where topk = 62 takes 17.)
 __device__ __forceinline__ bool too_close(uint32_t key, int n, int lane, float error)
 {
     const uint32_t after = __shfl_down(key, 1, 64);
@@ -723,7 +730,8 @@ __global__ __launch_bounds__(1024) void moe_place_kernel(SortArgs a)
                   [&](int i) { return a.ids[i]; });
 }
 
-// dx of w = scale p[ids] (or renormalised), a wave per token:
+// dx of w = scale p[ids] (or renormalised), a wave per token (8192 tokens, fp32,
+// top-8: 64 experts 5.2 us, 256 6.8, 512, which lanes store one by one, 15.5):
 //   softmax      dx = p (dp - <dp, p>), dp = scale dw at the chosen
 //   renormalised the same over the chosen alone
 //   sigmoid      dx = dw p (1 - p), renormalised (dw - <dw, r>) r (1 - p)

@@ -9,7 +9,7 @@
 //
 // Every set of that definition is a front part of one order, so a row needs
 // no sorting: only where in the order a count, a weight or a value is reached.
-// A row is read once.  Its values go to one of kBins bins of
+// A row is mostly read once.  Its values go to one of kBins bins of
 // (ref - x) / T, 1 / kPerUnit wide, each by one LDS addition that carries a
 // count and a weight, and those among the largest also to a list; ref and the
 // list's threshold come from a sample of the row.  Prefix sums over the bins
@@ -29,6 +29,10 @@
 // starts again with ref = the maximum.  A bin that holds more values than the
 // list (equal logits, a wide temperature) is narrowed down by further passes
 // over its keys, 4096 ways each; equal keys are counted by blocks of the row.
+// So two kinds of rows are read twice that need not be: at a low temperature one
+// with a winner outside of the sample, and one of which a wave samples nothing but
+// -infinity (a masked block): the threshold is then the lowest number, and the list
+// overflows.
 //
 // A workgroup takes a row, or one of `parts` of it where there are few rows;
 // then a second launch adds the parts' bins and finishes.
@@ -37,10 +41,15 @@
 // 13 where the list holds the answer and up to 42 for a flat row under top-p;
 // 256 fp32 rows of mixed options 85: 33 for the read (4.7 TB/s), then the
 // flattest row's second read 30 and its two searches 16; 48 rows of 50021 under
-// top-p 10 and 33.  Past the first read a row is a chain of short steps of one
-// workgroup.  (The second read over as many workgroups as the first: 26 us in
-// place of 36 for one row, but 29 in place of 21 for 48, the joining of the parts
-// taking 6.  More loads under way need registers that this kernel does not have.)
+// top-p 10 and 33.  With 24 likely tokens, T = 0.8 and top-p the second launch takes
+// 12 for one row, 18 with an eighth masked, and 23 at T = 0.2 with one value far
+// above; 256 rows 68, 86 and 62.  Past the first read a row is a chain of short
+// steps of one workgroup.  (The second read over as many workgroups as the first:
+// 26 us in place of 36 for one row, but 29 in place of 21 for 48, the joining of the
+// parts taking 6.)  The kernels that finish a row hold every search: 128 registers
+// and 15 to 28 more that are spilled (56 to 96 bytes a lane; the kernel that reads a
+// part takes 56 to 68), so that the second read has none for more loads, and 62 to
+// 66 KB of code, most of which a row fetches for the first time.
 #include "ffn_epilogue.h"
 #include "sample_internal.h"
 
